@@ -329,6 +329,90 @@ int scion_corr_forward(const void* v, int T, const scion_corr* corr, const float
  * a bounded wait of the tensor-core path gave up), like scion_layer_check. */
 int scion_corr_check(const scion_corr* corr, void* stream);
 
+/* ------------------------------------------------------ 8-bit dense operators
+ * The dense parts of a layer around the ternary block in 8-bit floating point: the residual add
+ * with its norm, the projections, and a dense (or shared-expert) SwiGLU feed-forward layer.  The
+ * pages keep these parts in 16 bits or more ("Scion-35B-A3B" model card, Weight Representation);
+ * these operators are an addition.  The container:
+ *   codes : e4m3 bytes (1 sign, 4 exponent bits of bias 7, 3 mantissa bits; largest 448; 0x7f /
+ *           0xff are NaN, there is no infinity), row-major;
+ *   scales: one byte b per block, the power of two 2^(b - 127) (E8M0; 255 is NaN).  A value is
+ *           code * scale.  A block is 128 consecutive columns of one row (activations, scales
+ *           [rows][ceil(cols/128)]) or 128 x 128 (weights, scales [ceil(rows/128)][ceil(cols/128)]);
+ *           the last block of a row or column may be shorter.
+ * Quantizing picks the smallest power of two s with max|v| / s <= 448 over the block (b clamped to
+ * >= 0; a block of zeros has b = 127) and rounds v / s to the nearest code, ties to even.  A block
+ * that holds an infinity or a NaN gets b = 255 and codes 0x7f, and every product it enters is NaN.
+ * Powers of two cost e4m3 no precision (its relative step does not depend on the scale), make
+ * every scaling exact, and are the scale type the tensor cores apply inside the product. */
+
+/* Element types of the dense operators. */
+enum { SCION_F32 = 0, SCION_BF16 = 1 };
+
+/* src: device [rows][cols] of src_type; block_rows: 1 (activations) or 128 (weights); codes and
+ * scales as above, device.  cols a multiple of 16, cols <= 2^20; rows >= 0 (rows = 0 is a no-op).
+ * src and codes 16-byte aligned.  EINVAL on a bad type, size, null or misaligned pointer; ECUDA. */
+int scion_fp8_quantize_device(int src_type, const void* src, int64_t rows, int cols, int block_rows, uint8_t* codes,
+                              uint8_t* scales, void* stream);
+
+/* The residual add and the root-mean-square norm in front of a sublayer:
+ *   r = x + resid;   resid_out = r;   y = r / sqrt(mean(r^2) + eps) * weight
+ * x: device [T][d] of x_type (a sublayer's output: fp32 as scion_moe_forward writes it, or bf16).
+ * resid: device [T][d] of resid_type or NULL (r = x).  resid_out: device [T][d] of resid_type or
+ * NULL (not written); it may be resid itself, or x itself where the types are the same.
+ * weight: device bf16 [d].  y_bf16: device bf16 [T][d] or NULL.  y_codes, y_scales: y in 8 bits
+ * with one scale per 128 columns, both or neither; at least one of resid_out, y_bf16 and y_codes
+ * is given.  r and the statistic are fp32, and the norm is taken of r before it is rounded to
+ * resid_type; the 8-bit output is quantized from the fp32 y.  A row that holds an infinity or a
+ * NaN, or whose sum of squares leaves the fp32 range, gives NaN in all of its y.  A row's result
+ * does not depend on the rows beside it.
+ * d a multiple of 16, d <= 32768; T >= 0 (T = 0 is a no-op); eps >= 0 and finite.  x, resid,
+ * resid_out, weight, y_bf16 and y_codes 16-byte aligned; no output may overlap another argument
+ * except as said.  EINVAL, ECUDA. */
+int scion_rmsnorm_forward(const void* x, int x_type, const void* resid, int resid_type, const void* weight, float eps,
+                          int T, int d, void* resid_out, void* y_bf16, uint8_t* y_codes, uint8_t* y_scales,
+                          void* stream);
+
+/* A dense layer with 8-bit weights: n outputs, k inputs, w_codes [n][k] with 128 x 128 scales
+ * w_scales [ceil(n/128)][ceil(k/128)] (scion_fp8_quantize_device with block_rows = 128).  With
+ * up_codes and up_scales (same shapes) the handle is a gated layer: w is the gate projection, up
+ * the up projection.  All of them are read in place and must outlive the handle.
+ * n >= 1, k a multiple of 16 and <= 65536, n <= 2^20; a gated layer's n is a multiple of 16.
+ * w_codes and up_codes 16-byte aligned.  EINVAL, ENOMEM, ECUDA. */
+typedef struct {
+  int n, k;
+  const uint8_t* w_codes;
+  const uint8_t* w_scales;
+  const uint8_t* up_codes;  /* NULL: a plain layer */
+  const uint8_t* up_scales;
+} scion_fp8_desc;
+typedef struct scion_fp8 scion_fp8;
+int scion_fp8_create(const scion_fp8_desc* desc, void* stream, scion_fp8** out);
+void scion_fp8_destroy(scion_fp8* layer);
+/* Bytes of device memory the handle owns (its status word; the weights are the caller's). */
+size_t scion_fp8_device_bytes(const scion_fp8* layer);
+
+/* out[t] = base[t] + W x_t for a plain layer: x in 8 bits (x_codes [T][k], x_scales
+ * [T][ceil(k/128)]), out device [T][n] of out_type (SCION_F32 or SCION_BF16), base device fp32
+ * [T][n] or NULL; with out_type SCION_F32 it may be out itself.  Products and sums in fp32, one
+ * rounding to out_type.  A row's result is bit-reproducible for the same T and does not depend on
+ * the other rows.  T >= 0 (T = 0 is a no-op).  x_codes 16-byte aligned, out and base aligned to
+ * their elements.  The handle holds no workspace: calls on one handle may overlap.  EINVAL (also
+ * for a gated layer), ECUDA. */
+int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* layer, const float* base,
+                      void* out, int out_type, void* stream);
+
+/* h_t = silu(W_gate x_t) * (W_up x_t) of a gated layer in one kernel: h_bf16 device bf16 [T][n] or
+ * NULL; h_codes [T][n] and h_scales [T][ceil(n/128)], both or neither (quantized from the fp32 h,
+ * ready as the x of the down projection); one of the two forms is given, not both.  h_bf16 and
+ * h_codes 16-byte aligned.  Otherwise as scion_fp8_forward; EINVAL for a plain layer. */
+int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* layer,
+                            void* h_bf16, uint8_t* h_codes, uint8_t* h_scales, void* stream);
+
+/* Waits for `stream`, then returns and clears the handle's device status word (SCION_ETIMEOUT if a
+ * bounded wait of an earlier forward gave up; its output is then invalid), like scion_layer_check. */
+int scion_fp8_check(const scion_fp8* layer, void* stream);
+
 /* ------------------------------------------------------------ measurement
  * Kernel-level timing for benchmarks.  Between scion_profile_begin and
  * scion_profile_end, every kernel a forward launches is bracketed by a pair of CUDA

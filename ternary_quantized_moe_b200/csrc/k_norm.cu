@@ -1,0 +1,242 @@
+// k_norm.cu -- the residual add with its root-mean-square norm, and the float -> e4m3 quantizers
+// (rows x 128 for activations, 128 x 128 for weights).  Entry points at the end of the file.
+//
+// All three are bound by HBM: one read of every input, one write of every output, nothing kept in
+// memory in between.  A thread holds 8 consecutive columns (16 bytes of bf16, 32 of fp32 per load
+// and lane), so a group of 128 columns is half a warp and its largest magnitude one redux over 16
+// lanes; the loads of a warp cover whole 32-byte sectors.
+#include <math.h>
+
+#include <algorithm>
+
+#include "fp8_common.cuh"
+#include "scion_internal.cuh"
+
+namespace scion {
+namespace {
+
+using namespace fp8;
+typedef __nv_bfloat16 bf16;
+
+// Largest magnitude of the half warp the lane is in (all 32 lanes take part).
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
+  const uint32_t mask = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
+  return __reduce_max_sync(mask, m);
+}
+__device__ __forceinline__ uint32_t mag8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, mag(v[i]));
+  return m;
+}
+__device__ __forceinline__ uint2 code8(const float (&v)[8], float inv) {
+  return make_uint2(pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+
+// ------------------------------------------------------------------ norm
+struct NormParams {
+  const void* x;
+  const void* resid;
+  const bf16* w;
+  void* resid_out;
+  bf16* y;
+  uint8_t* codes;
+  uint8_t* scales;
+  float eps;
+  int d, groups;
+};
+
+// One CTA per row; thread t holds the 8-column chunks t, t + blockDim, ...: the row stays in
+// registers between the statistic and the output.
+template <typename X, typename R, int CPT>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
+  __shared__ float part[32];
+  const int64_t row = int64_t(blockIdx.x) * p.d;
+  const int chunks = p.d >> 3, nt = blockDim.x;
+  float v[CPT][8];
+  uint4 w[CPT];  // the weights' loads are in flight with the row's
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = threadIdx.x + i * nt;
+    if (c < chunks) {
+      w[i] = __ldg(reinterpret_cast<const uint4*>(p.w + 8 * c));
+      load8(static_cast<const X*>(p.x) + row + 8 * c, v[i]);
+      if (p.resid) {
+        float r[8];
+        load8(static_cast<const R*>(p.resid) + row + 8 * c, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = nt >> 5;
+  if (lane == 0) part[warp] = ss;
+  __syncthreads();
+  ss = lane < nw ? part[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  // an infinite sum would turn the row's finite elements into zeros: the whole row is NaN instead
+  const float rms = ss < INFINITY ? rsqrtf(ss / float(p.d) + p.eps) : NAN;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = threadIdx.x + i * nt;
+    const bool in = c < chunks;
+    if (in && p.resid_out) store8(static_cast<R*>(p.resid_out) + row + 8 * c, v[i]);
+    if (!p.y && !p.codes) continue;
+    if (in) {
+      float wf[8];
+      unpack_bf16x8(w[i], wf);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rms * wf[j];
+      if (p.y) store8(p.y + row + 8 * c, v[i]);
+    }
+    if (p.codes) {
+      const uint32_t b = scale_byte(half_warp_max(in ? mag8(v[i]) : 0u));
+      if (in) *reinterpret_cast<uint2*>(p.codes + row + 8 * c) = code8(v[i], scale_inverse(b));
+      if (in && (threadIdx.x & 15) == 0) p.scales[int64_t(blockIdx.x) * p.groups + (c >> 4)] = uint8_t(b);
+    }
+  }
+}
+
+template <typename X, typename R>
+cudaError_t launch_norm(const NormParams& p, int T, cudaStream_t s) {
+  const int chunks = p.d >> 3;
+  const int cpt = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  const int nt = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
+  if (cpt == 1) rmsnorm_kernel<X, R, 1><<<T, nt, 0, s>>>(p);
+  else if (cpt == 2) rmsnorm_kernel<X, R, 2><<<T, nt, 0, s>>>(p);
+  else rmsnorm_kernel<X, R, 4><<<T, nt, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ quantizers
+// Activations: a half warp per group of 128 columns of a row.
+template <typename S>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const S* __restrict__ src, int64_t rows, int cols,
+                                                            int groups, uint8_t* __restrict__ codes,
+                                                            uint8_t* __restrict__ scales) {
+  const int64_t n = rows * groups;
+  const int64_t per = int64_t(gridDim.x) * 16;
+  // the two half warps of a warp walk neighbouring groups; the bound is rounded up to whole warps
+  for (int64_t g = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4); g < (n + 1) / 2 * 2; g += per) {
+    const int64_t row = g / groups;
+    const int c0 = int(g - row * groups) * 128 + 8 * (threadIdx.x & 15);
+    const bool in = g < n && c0 < cols;
+    float v[8] = {};
+    if (in) load8(src + row * cols + c0, v);
+    const uint32_t b = scale_byte(half_warp_max(mag8(v)));
+    if (in) *reinterpret_cast<uint2*>(codes + row * cols + c0) = code8(v, scale_inverse(b));
+    if (g < n && (threadIdx.x & 15) == 0) scales[g] = uint8_t(b);
+  }
+}
+
+// Weights: a CTA per 128 x 128 block, 8 x 8 values per thread in registers.
+template <typename S>
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(const S* __restrict__ src, int64_t rows, int cols,
+                                                              int groups, uint8_t* __restrict__ codes,
+                                                              uint8_t* __restrict__ scales) {
+  __shared__ uint32_t part[8];
+  const int64_t rb = blockIdx.x / groups;
+  const int g = int(blockIdx.x - rb * groups);
+  const int c = g * 128 + 8 * (threadIdx.x & 15);
+  const int64_t r0 = rb * 128 + (threadIdx.x >> 4);
+  float v[8][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + 16 * i;
+    if (r < rows && c < cols) {
+      load8(src + r * cols + c, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, mag8(v[i]));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+  const uint32_t b = scale_byte(m);
+  const float inv = scale_inverse(b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + 16 * i;
+    if (r < rows && c < cols) *reinterpret_cast<uint2*>(codes + r * cols + c) = code8(v[i], inv);
+  }
+  if (threadIdx.x == 0) scales[blockIdx.x] = uint8_t(b);
+}
+
+template <typename S>
+cudaError_t launch_quantize(const S* src, int64_t rows, int cols, int block_rows, uint8_t* codes, uint8_t* scales,
+                            cudaStream_t s) {
+  const int groups = (cols + 127) / 128;
+  if (block_rows == 1) {
+    const int64_t ctas = (rows * groups + 15) / 16;
+    quantize_rows_kernel<S><<<unsigned(std::min<int64_t>(ctas, 1 << 20)), 256, 0, s>>>(src, rows, cols, groups, codes,
+                                                                                      scales);
+  } else {
+    quantize_blocks_kernel<S><<<unsigned((rows + 127) / 128 * groups), 256, 0, s>>>(src, rows, cols, groups, codes,
+                                                                                   scales);
+  }
+  return cudaGetLastError();
+}
+
+inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+}  // namespace
+}  // namespace scion
+
+extern "C" int scion_fp8_quantize_device(int src_type, const void* src, int64_t rows, int cols, int block_rows,
+                                         uint8_t* codes, uint8_t* scales, void* stream) {
+  if ((src_type != SCION_F32 && src_type != SCION_BF16) || (block_rows != 1 && block_rows != 128)) return SCION_EINVAL;
+  if (rows < 0 || cols < 16 || cols % 16 || cols > (1 << 20)) return SCION_EINVAL;
+  // one CTA per 128 x 128 block: the grid stays within 2^31 - 1
+  if (rows > (int64_t(1) << 40) || (block_rows == 128 && (rows + 127) / 128 * ((cols + 127) / 128) > 0x7fffffff))
+    return SCION_EINVAL;
+  if (rows == 0) return SCION_OK;
+  if (!src || !codes || !scales || scion::misaligned(src, 16) || scion::misaligned(codes, 16)) return SCION_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      src_type == SCION_F32
+          ? scion::launch_quantize(static_cast<const float*>(src), rows, cols, block_rows, codes, scales, s)
+          : scion::launch_quantize(static_cast<const __nv_bfloat16*>(src), rows, cols, block_rows, codes, scales, s);
+  return e == cudaSuccess ? SCION_OK : SCION_ECUDA;
+}
+
+extern "C" int scion_rmsnorm_forward(const void* x, int x_type, const void* resid, int resid_type, const void* weight,
+                                     float eps, int T, int d, void* resid_out, void* y_bf16, uint8_t* y_codes,
+                                     uint8_t* y_scales, void* stream) {
+  if ((x_type != SCION_F32 && x_type != SCION_BF16) || (resid_type != SCION_F32 && resid_type != SCION_BF16))
+    return SCION_EINVAL;
+  if (T < 0 || d < 16 || d % 16 || d > 32768 || !(eps >= 0.f) || !isfinite(eps)) return SCION_EINVAL;
+  if (!y_codes != !y_scales || (!resid_out && !y_bf16 && !y_codes)) return SCION_EINVAL;
+  if (T == 0) return SCION_OK;
+  if (!x || !weight) return SCION_EINVAL;
+  for (const void* p : {x, resid, weight, static_cast<const void*>(resid_out), static_cast<const void*>(y_bf16),
+                        static_cast<const void*>(y_codes)})
+    if (scion::misaligned(p, 16)) return SCION_EINVAL;
+  // in place on x only where an element is as wide (a thread then overwrites what it alone has read)
+  if (resid_out == x && resid_type != x_type) return SCION_EINVAL;
+  scion::NormParams p{x,       resid,    static_cast<const __nv_bfloat16*>(weight), resid_out, static_cast<__nv_bfloat16*>(y_bf16),
+                      y_codes, y_scales, eps, d, (d + 127) / 128};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  using scion::launch_norm;
+  const cudaError_t e = x_type == SCION_F32
+                            ? (resid_type == SCION_F32 ? launch_norm<float, float>(p, T, s)
+                                                       : launch_norm<float, __nv_bfloat16>(p, T, s))
+                            : (resid_type == SCION_F32 ? launch_norm<__nv_bfloat16, float>(p, T, s)
+                                                       : launch_norm<__nv_bfloat16, __nv_bfloat16>(p, T, s));
+  return e == cudaSuccess ? SCION_OK : SCION_ECUDA;
+}
