@@ -1,15 +1,20 @@
 // k_fp8.cu -- matrix products in e4m3 with one power-of-two scale per 128 columns (activations) or
 // 128 x 128 block (weights): the plain layer and the gated layer.
 //
-// A plain tiled kernel: codes expanded to fp32 times their scale in shared memory, fp32 FMAs.
+// Both run on tcgen05.mma kind::mxf8f6f4: the tensor cores multiply e4m3 operands and apply the
+// E8M0 scales themselves (a scale byte per row and 32 columns; the four steps of a 128-column block
+// use the same byte), so nothing is expanded or promoted outside them.
 #include <algorithm>
 #include <new>
 
 #include "fp8_common.cuh"
 #include "scion_internal.cuh"
+#include "tc_common.cuh"
 
 struct scion_fp8 {
   scion_fp8_desc desc;
+  CUtensorMap w[2];
+  int sms;
   int* err;  // device status word
   size_t device_bytes;
 };
@@ -18,108 +23,295 @@ namespace scion {
 namespace {
 
 using namespace fp8;
+using namespace tc;
 typedef __nv_bfloat16 bf16;
 
-__device__ __forceinline__ float value(uint8_t code) {
-  __nv_fp8_e4m3 v;
-  v.__x = code;
-  return float(v);
-}
+// ------------------------------------------------------------------ streaming kernel
+// Few tokens: bound by reading the weights once.  The weights are the M side (128 rows per tile),
+// the tokens the N side (bn of them, a multiple of 16), and the CTAs of a cluster split K, so that a
+// matrix of few tiles still spreads over the SMs; their partial sums meet in distributed shared
+// memory and are added in rank order.  Roles: warp 0 TMA loads through a ring of 128-column stages,
+// warp 1 the MMAs, warps 2..5 the scale words (global -> tensor memory) and the epilogue.
+constexpr int kStreamThreads = 192;
+constexpr int kMaxStages = 12;
+constexpr int kSfSlots = 4;  // ring of scale words, each slot for 4 K blocks (one byte each)
+constexpr uint32_t kSmem = 227 * 1024;
 
-struct Fp8Params {
-  const uint8_t* x;
-  const uint8_t* sx;
-  const uint8_t* w[2];
+struct StreamParams {
+  CUtensorMap w[2], x;
   const uint8_t* sw[2];
+  const uint8_t* sx;
   const float* base;
-  void* out;  // plain: out of out_type; gated: bf16 h
+  void* out;
   uint8_t* codes;
   uint8_t* scales;
-  int T, N, K, KB, out_bf16;
+  int* err;
+  int T, N, KB;
+  int bn, stages, tmem_cols, sf_col, sfb_cols;
+  int out_bf16, vec, sf_vec;
 };
 
-constexpr int kTT = 32, kTK = 32;
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages], sf_full[kSfSlots], sf_empty[kSfSlots], acc_full, done;
+  uint32_t tmem_slot;
+  int abort_flag;
+};
 
-template <int NW>
-__global__ void __launch_bounds__(256) fp8_simple_kernel(const Fp8Params p) {
-  __shared__ float xs[kTT][kTK + 1], ws[NW][128][kTK + 1];
-  const int n0 = blockIdx.x * 128, t0 = blockIdx.y * kTT;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  float acc[NW][4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += kTK) {
-    const int kb = k0 / 128;
-    for (int i = threadIdx.x; i < kTT * kTK; i += 256) {
-      const int t = t0 + i / kTK, k = k0 + i % kTK;
-      xs[i / kTK][i % kTK] =
-          t < p.T && k < p.K ? value(p.x[int64_t(t) * p.K + k]) * scale_value(p.sx[int64_t(t) * p.KB + kb]) : 0.f;
-    }
+// Scale bytes of K blocks 4q .. 4q + 3 of one row; blocks past the end read as 2^0.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int q, int KB, bool vec) {
+  if (vec) return *reinterpret_cast<const uint32_t*>(row + 4 * q);
+  uint32_t w = 0x7f7f7f7fu;
 #pragma unroll
-    for (int m = 0; m < NW; ++m)
-      for (int i = threadIdx.x; i < 128 * kTK; i += 256) {
-        const int n = n0 + i / kTK, k = k0 + i % kTK;
-        ws[m][i / kTK][i % kTK] = n < p.N && k < p.K ? value(p.w[m][int64_t(n) * p.K + k]) *
-                                                          scale_value(p.sw[m][int64_t(blockIdx.x) * p.KB + kb])
-                                                     : 0.f;
-      }
-    __syncthreads();
-#pragma unroll 4
-    for (int k = 0; k < kTK; ++k)
-#pragma unroll
-      for (int m = 0; m < NW; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[m][i][j] = fmaf(xs[ty + 8 * i][k], ws[m][tx + 32 * j][k], acc[m][i][j]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + ty + 8 * i;
-    if (t >= p.T) break;  // (whole warps: a warp's tokens are its ty)
-    float h[4];
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = acc[0][i][j];
-      h[j] = NW == 2 ? a / (1.f + __expf(-a)) * acc[NW - 1][i][j] : a;
-      if (n0 + tx + 32 * j < p.N) m = max(m, mag(h[j]));
-    }
-    const uint32_t b = scale_byte(__reduce_max_sync(0xffffffffu, m));
-    if (NW == 2 && p.codes && tx == 0) p.scales[int64_t(t) * ((p.N + 127) / 128) + blockIdx.x] = uint8_t(b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx + 32 * j;
-      if (n >= p.N) continue;
-      const int64_t at = int64_t(t) * p.N + n;
-      if (NW == 2 && p.codes) {
-        p.codes[at] = uint8_t(pack4(h[j] * scale_inverse(b), 0.f, 0.f, 0.f));
-      } else {
-        const float v = NW == 1 && p.base ? p.base[at] + h[j] : h[j];
-        if (p.out_bf16) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(v);
-        else static_cast<float*>(p.out)[at] = v;
-      }
-    }
-  }
+  for (int i = 0; i < 4; ++i)
+    if (4 * q + i < KB) w = (w & ~(0xffu << (8 * i))) | (uint32_t(row[4 * q + i]) << (8 * i));
+  return w;
 }
 
-cudaError_t launch_fp8(const Fp8Params& p, int gated, cudaStream_t s) {
-  const dim3 grid((p.N + 127) / 128, (p.T + kTT - 1) / kTT);
-  if (gated) fp8_simple_kernel<2><<<grid, 256, 0, s>>>(p);
-  else fp8_simple_kernel<1><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+__device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
+// NW = 1: out = base + W x.  NW = 2: h = silu(W0 x) (W1 x), to bf16 or codes and scales.
+template <int NW>
+__global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid_constant__ StreamParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars& bars = *reinterpret_cast<Bars*>(smem);
+  uint8_t* ring = smem + 1024;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x, splits = gridDim.x;
+  const int row0 = blockIdx.y * 128, tok0 = blockIdx.z * p.bn;
+  const int kb0 = int(int64_t(rank) * p.KB / splits), kb1 = int(int64_t(rank + 1) * p.KB / splits);
+  const uint32_t stage_bytes = NW * 16384 + p.bn * 128;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(&bars.full[s], 1), mbar_init(&bars.empty[s], 1);
+    for (int s = 0; s < kSfSlots; ++s) mbar_init(&bars.sf_full[s], 128), mbar_init(&bars.sf_empty[s], 1);
+    mbar_init(&bars.acc_full, 1), mbar_init(&bars.done, 1);
+    bars.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(&bars.tmem_slot, p.tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_slot;
+  volatile int* abort_flag = &bars.abort_flag;
+  pdl_trigger();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
+        const int s = i % p.stages;
+        if (i >= p.stages && !mbar_wait(&bars.empty[s], (i / p.stages - 1) & 1, abort_flag, p.err)) break;
+        uint8_t* st = ring + s * stage_bytes;
+        mbar_arrive_expect_tx(&bars.full[s], stage_bytes);
+        tma_load_2d(st, &p.w[0], kb * 128, row0, &bars.full[s]);
+        if (NW == 2) tma_load_2d(st + 16384, &p.w[1], kb * 128, row0, &bars.full[s]);
+        tma_load_2d(st + NW * 16384, &p.x, kb * 128, tok0, &bars.full[s]);
+      }
+      // copies may still be in flight if the MMA warp gave up
+      for (int j = max(0, i - p.stages); j < i; ++j) mbar_drain(&bars.full[j % p.stages], (j / p.stages) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int i = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1 && ok; ++kb, ++i) {
+        const int s = i % p.stages, q = kb / 4 - kb0 / 4, slot = q % kSfSlots;
+        if (kb == kb0 || (kb & 3) == 0) ok = mbar_wait(&bars.sf_full[slot], (q / kSfSlots) & 1, abort_flag, p.err);
+        ok = ok && mbar_wait(&bars.full[s], (i / p.stages) & 1, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(ring + s * stage_bytes);
+        const uint32_t sf = tmem + p.sf_col + slot * (4 * NW + p.sfb_cols);
+        const uint32_t idesc = umma_idesc_mx8(128, p.bn, kb & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t db = umma_desc_sw128(st + NW * 16384 + 32 * k);
+#pragma unroll
+          for (int m = 0; m < NW; ++m)
+            umma_mx8(tmem + m * p.bn, umma_desc_sw128(st + m * 16384 + 32 * k), db, idesc, sf + 4 * m, sf + 4 * NW,
+                     (i | k) != 0);
+        }
+        umma_commit(&bars.empty[s]);
+        if ((kb & 3) == 3) umma_commit(&bars.sf_empty[slot]);
+      }
+      if (ok) umma_commit(&bars.acc_full);
+      // every MMA issued above has finished before shared and tensor memory are reused
+      umma_commit(&bars.done);
+      mbar_drain(&bars.done, 0);
+    }
+  } else {
+    // scale words: each of the four warps writes them to its own lane quarter
+    const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
+    const int q0 = kb0 / 4, nq = (kb1 - 1) / 4 - q0 + 1;
+    bool ok = true;
+    for (int i = 0; i < nq; ++i) {
+      const int slot = i % kSfSlots, q = q0 + i;
+      uint32_t wa[NW], wb[8];
+#pragma unroll
+      for (int m = 0; m < NW; ++m) wa[m] = scale_word(p.sw[m] + int64_t(blockIdx.y) * p.KB, q, p.KB, p.sf_vec);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int t = tok0 + 32 * c + lane;
+        wb[c] = 32 * c < p.bn && t < p.T ? scale_word(p.sx + int64_t(t) * p.KB, q, p.KB, p.sf_vec) : 0x7f7f7f7fu;
+      }
+      if (i >= kSfSlots) {
+        ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (i / kSfSlots - 1) & 1, abort_flag, p.err));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t sf = tmem + quarter + p.sf_col + slot * (4 * NW + p.sfb_cols);
+#pragma unroll
+      for (int m = 0; m < NW; ++m) tmem_st4(sf + 4 * m, wa[m], wa[m], wa[m], wa[m]);
+      tmem_st4(sf + 4 * NW, wb[0], wb[1], wb[2], wb[3]);
+      if (p.sfb_cols > 4) tmem_st4(sf + 4 * NW + 4, wb[4], wb[5], wb[6], wb[7]);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bars.sf_full[slot]);
+    }
+    // partial sums to shared memory [matrix][token][128 features] (the ring is free: every load has
+    // been read by an MMA, and every MMA has finished)
+    if (ok && named_bar_and(1, 128, mbar_wait(&bars.acc_full, 0, abort_flag, p.err))) {
+      tc_fence_after();
+      float* part = reinterpret_cast<float*>(ring) + (warp & 3) * 32 + lane;
+      for (int c = 0; c < NW * p.bn; c += 16) {
+        float v[16];
+        tmem_ld16(tmem + quarter + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[(c + i) * 128] = v[i];
+      }
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (splits > 1) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+
+  // tokens rank, rank + splits, ... of the tile: a warp per token, 4 features per lane
+  const int nt = min(p.bn, p.T - tok0);
+  const int n = row0 + 4 * lane;
+  const uint32_t mine = smem_u32(ring) + 16 * lane;
+  for (int t = rank + splits * warp; t < nt; t += splits * (kStreamThreads / 32)) {
+    float v[NW][4];
+#pragma unroll
+    for (int m = 0; m < NW; ++m) {
+      const uint32_t at = mine + uint32_t(m * p.bn + t) * 512;
+      float4 s = ld_dsmem_f4(map_cluster_rank(at, 0));
+      for (int r = 1; r < splits; ++r) {
+        const float4 o = ld_dsmem_f4(map_cluster_rank(at, r));
+        s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+      }
+      v[m][0] = s.x, v[m][1] = s.y, v[m][2] = s.z, v[m][3] = s.w;
+    }
+    const int64_t tok = tok0 + t, at = tok * p.N + n;
+    if (NW == 1) {
+      if (p.vec && n < p.N) {  // N a multiple of 4, rows aligned: all four or none
+        if (p.base) {
+          const float4 b = *reinterpret_cast<const float4*>(p.base + at);
+          v[0][0] += b.x, v[0][1] += b.y, v[0][2] += b.z, v[0][3] += b.w;
+        }
+        if (p.out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<bf16*>(p.out) + at) =
+              make_uint2(pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (n + j >= p.N) continue;
+          const float o = (p.base ? p.base[at + j] : 0.f) + v[0][j];
+          if (p.out_bf16) static_cast<bf16*>(p.out)[at + j] = __float2bfloat16_rn(o);
+          else static_cast<float*>(p.out)[at + j] = o;
+        }
+      }
+    } else {
+      float h[4];
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = silu_mul(v[0][j], v[NW - 1][j]), m = max(m, n < p.N ? mag(h[j]) : 0u);
+      if (p.codes) {
+        const uint32_t b = scale_byte(__reduce_max_sync(0xffffffffu, m));
+        const float inv = scale_inverse(b);
+        if (n < p.N) *reinterpret_cast<uint32_t*>(p.codes + at) = pack4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+        if (lane == 0) p.scales[tok * ((p.N + 127) / 128) + blockIdx.y] = uint8_t(b);
+      } else if (n < p.N) {
+        *reinterpret_cast<uint2*>(static_cast<bf16*>(p.out) + at) =
+            make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+      }
+    }
+  }
+  if (splits > 1) cluster_sync();  // the other CTAs may still be reading this one's sums
+}
+
+// ------------------------------------------------------------------ host side
+inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// Tensor map of an e4m3 matrix [rows][K]: boxes of 128 columns x box_rows, 128-byte swizzle.
+int make_tmap_codes(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, int box_rows) {
+  const auto fn = encode_tiled_fn();
+  if (!fn) return SCION_ECUDA;
+  cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(K)};
+  cuuint32_t box[2] = {128, cuuint32_t(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SCION_OK : SCION_ECUDA;
 }
 
 int status(cudaError_t e) {
   return e == cudaSuccess ? SCION_OK : e == cudaErrorMemoryAllocation ? SCION_ENOMEM : SCION_ECUDA;
 }
-inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
-Fp8Params params(const scion_fp8* L, const uint8_t* x, const uint8_t* sx, int T) {
-  Fp8Params p{};
-  p.x = x, p.sx = sx;
-  p.w[0] = L->desc.w_codes, p.sw[0] = L->desc.w_scales;
-  p.w[1] = L->desc.up_codes, p.sw[1] = L->desc.up_scales;
-  p.T = T, p.N = L->desc.n, p.K = L->desc.k, p.KB = (p.K + 127) / 128;
+template <int NW>
+int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, cudaStream_t s) {
+  p.w[0] = L->w[0], p.w[1] = L->w[NW - 1];
+  // tokens of a tile: the accumulators (NW bn columns) and the scale words share 512 columns
+  const int most = NW == 1 ? 256 : 208;
+  const int t_tiles = (T + most - 1) / most;
+  p.bn = ((T + t_tiles - 1) / t_tiles + 15) / 16 * 16;
+  const int n_tiles = (p.N + 127) / 128;
+  const int splits = std::max(1, std::min({8, p.KB, L->sms / (n_tiles * t_tiles)}));
+  p.sfb_cols = p.bn > 128 ? 8 : 4;
+  p.sf_col = (NW * p.bn + 3) / 4 * 4;
+  p.tmem_cols = int(tmem_cols_pow2(p.sf_col + kSfSlots * (4 * NW + p.sfb_cols)));
+  // Shared memory in step with tensor memory: CTAs that fit an SM together by the one then fit by
+  // the other too, so no CTA of a cluster can wait for tensor memory held by a CTA that waits for
+  // its own cluster.
+  const uint32_t share = 228 * 1024 / 512 * p.tmem_cols - 1024;
+  const uint32_t stage = NW * 16384 + p.bn * 128;
+  const uint32_t budget = std::max<uint32_t>(share, 113 * 1024);
+  p.stages = std::min<int>({kMaxStages, int((budget - 2048) / stage), (p.KB + splits - 1) / splits});
+  p.stages = std::max(p.stages, 1);
+  const uint32_t need = 2048 + std::max<uint32_t>(p.stages * stage, NW * p.bn * 512);
+  const uint32_t smem = std::max(need, share);
+  if (smem > kSmem) return SCION_EINVAL;
+  int st = make_tmap_codes(&p.x, x, T, L->desc.k, p.bn);
+  if (st != SCION_OK) return st;
+  return status(launch_pdl_cluster(fp8_stream_kernel<NW>, dim3(splits, n_tiles, t_tiles), dim3(kStreamThreads),
+                                   dim3(splits, 1, 1), smem, s, p));
+}
+
+StreamParams params(const scion_fp8* L, const uint8_t* sx, int T) {
+  StreamParams p{};
+  p.sx = sx, p.sw[0] = L->desc.w_scales, p.sw[1] = L->desc.up_scales;
+  p.T = T, p.N = L->desc.n, p.KB = (L->desc.k + 127) / 128, p.err = L->err;
+  p.sf_vec = p.KB % 4 == 0 && !misaligned(sx, 4) && !misaligned(p.sw[0], 4) && !misaligned(p.sw[1], 4);
   return p;
 }
 
@@ -138,7 +330,19 @@ extern "C" int scion_fp8_create(const scion_fp8_desc* D, void* stream, scion_fp8
   L->desc = *D;
   L->err = nullptr;
   L->device_bytes = sizeof(int);
-  cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&L->err), sizeof(int));
+  int st = scion::make_tmap_codes(&L->w[0], D->w_codes, D->n, D->k, 128);
+  if (st == SCION_OK && D->up_codes) st = scion::make_tmap_codes(&L->w[1], D->up_codes, D->n, D->k, 128);
+  if (st != SCION_OK) {
+    delete L;
+    return st;
+  }
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&L->sms, cudaDevAttrMultiProcessorCount, dev);
+  // (a function attribute of the current device)
+  for (const auto f : {scion::fp8_stream_kernel<1>, scion::fp8_stream_kernel<2>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, scion::kSmem);
+  if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&L->err), sizeof(int));
   if (e == cudaSuccess) e = cudaMemsetAsync(L->err, 0, sizeof(int), static_cast<cudaStream_t>(stream));
   // (the word is cleared before a forward on another stream can run)
   if (e == cudaSuccess) e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
@@ -165,9 +369,10 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
   if (!x_codes || !x_scales || !out || scion::misaligned(x_codes, 16)) return SCION_EINVAL;
   if (scion::misaligned(base, 4) || scion::misaligned(out, out_type == SCION_F32 ? 4 : 2)) return SCION_EINVAL;
   if (out_type == SCION_BF16 && static_cast<const void*>(base) == out && base) return SCION_EINVAL;
-  scion::Fp8Params p = scion::params(L, x_codes, x_scales, T);
+  scion::StreamParams p = scion::params(L, x_scales, T);
   p.base = base, p.out = out, p.out_bf16 = out_type == SCION_BF16;
-  return scion::status(scion::launch_fp8(p, 0, static_cast<cudaStream_t>(stream)));
+  p.vec = p.N % 4 == 0 && !scion::misaligned(base, 16) && !scion::misaligned(out, 16);
+  return scion::launch_stream<1>(L, p, x_codes, T, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* L,
@@ -178,9 +383,9 @@ extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_
   if (!x_codes || !x_scales || scion::misaligned(x_codes, 16) || scion::misaligned(h_bf16, 16) ||
       scion::misaligned(h_codes, 16))
     return SCION_EINVAL;
-  scion::Fp8Params p = scion::params(L, x_codes, x_scales, T);
-  p.out = h_bf16, p.out_bf16 = 1, p.codes = h_codes, p.scales = h_scales;
-  return scion::status(scion::launch_fp8(p, 1, static_cast<cudaStream_t>(stream)));
+  scion::StreamParams p = scion::params(L, x_scales, T);
+  p.out = h_bf16, p.codes = h_codes, p.scales = h_scales;
+  return scion::launch_stream<2>(L, p, x_codes, T, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int scion_fp8_check(const scion_fp8* L, void* stream) {

@@ -25,7 +25,7 @@
 //   PQ2_0 : inside every 16 columns, position 2s+h holds column s + 8h (s < 8, h < 2)
 //   PTQ1_0: each 64-column half of a 128-column group is self-contained: quintets 12h..12h+11
 //           in pairs, then remainder trits 4h..4h+3 (see perm_pos).
-#include <cudaTypedefs.h>
+
 #include <float.h>
 #include <math.h>
 
@@ -932,9 +932,7 @@ __global__ void __launch_bounds__(256) group_scatter_kernel(const int32_t* __res
 // ====================================================================== host side
 namespace scion {
 
-namespace {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     void* p = nullptr;
@@ -945,6 +943,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   }
   return fn;
 }
+
+namespace {
 
 int num_sms() {
   static int n = 0;
@@ -983,7 +983,7 @@ constexpr size_t kDenseSmem = kDenseStages * kDenseStage + 1024;
 
 // K-major [rows][K] 2-byte matrix, box {64 columns, box_rows rows}, 128-byte swizzle.
 int make_tmap_2d(CUtensorMap* map, const void* ptr, int bf16, int64_t rows, int64_t K, int box_rows) {
-  auto fn = encode_fn();
+  auto fn = encode_tiled_fn();
   if (!fn) return SCION_ECUDA;
   if ((reinterpret_cast<uintptr_t>(ptr) & 15) || (K * 2) % 16) return SCION_EINVAL;
   cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};

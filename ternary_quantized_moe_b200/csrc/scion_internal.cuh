@@ -27,6 +27,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -231,6 +232,7 @@ cudaError_t launch_corr_prefill(const CorrState* C, const __nv_bfloat16* v, int 
                                 cudaStream_t s);
 
 // k_prefill.cu
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled_fn();  // the driver's encoder, or nullptr
 int make_tmap_2d(CUtensorMap* map, const void* ptr, int bf16, int64_t rows, int64_t K, int box_rows = 128);
 // k_tdec.cu: expert gate/up (na = 2) or down (na = 1, gate-weighted fp32 reductions into out) of
 // a decode batch on the tensor cores, tiles of up to kDecTile tokens listed by the routing.

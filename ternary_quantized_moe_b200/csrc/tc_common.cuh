@@ -201,6 +201,25 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       : "memory");
 }
 
+// 8-bit block-scaled form: instruction descriptor of kind::mxf8f6f4 with e4m3 A and B, fp32
+// accumulate, K-major operands and E8M0 scales; sf_id selects the byte of the scale words (one byte
+// per row and K step of 32) that this step reads, for A and B alike.
+__host__ __device__ constexpr uint32_t umma_idesc_mx8(int M, int N, int sf_id) {
+  return (uint32_t(sf_id) << 4) | (uint32_t(N >> 3) << 17) | (1u << 23) | (uint32_t(M >> 4) << 24) |
+         (uint32_t(sf_id) << 29);
+}
+// D += (A scaled) (B scaled)^T over one K step of 32.  Scale words in tensor memory: row r of A (or B)
+// in lane r % 32 (the same in all four lane quarters), column sf + r / 32.
+__device__ __forceinline__ void umma_mx8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on `bar` when all prior tcgen05.mma of this thread have completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -266,9 +285,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// 32 lanes x 4 consecutive columns.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ uint32_t tmem_cols_pow2(uint32_t n) {
+__host__ __device__ __forceinline__ uint32_t tmem_cols_pow2(uint32_t n) {
   uint32_t c = 32;
   while (c < n) c <<= 1;
   return c;
