@@ -257,6 +257,302 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
   if (splits > 1) cluster_sync();  // the other CTAs may still be reading this one's sums
 }
 
+// ------------------------------------------------------------------ pair kernel
+// Many tokens: bound by the tensor cores.  A pair of CTAs (cta_group::2) computes 256 tokens x 256
+// weight rows: tokens are the M side, 128 per CTA, so that a thread of the epilogue holds one token's
+// row of consecutive features (a group's largest magnitude needs no exchange beyond two threads), and
+// each CTA loads half of the weight rows, which halves the shared-memory traffic of B.  A gated tile
+// is 128 gate rows (first CTA) and the 128 up rows of the same features (second CTA).  Persistent:
+// the pairs walk the tiles in groups of 8 token tiles, so that the operands in use stay in L2.
+// Roles: warp 0 TMA loads, warp 1 the MMAs (first CTA only), warps 2..5 the scale words, warps 6..13
+// the epilogue (two per lane quarter, each half of the 256 columns).  The 256 accumulator columns
+// are drained into registers and released before anything is stored, so the next tile's MMAs wait
+// for the drain alone.
+constexpr int kPairThreads = 14 * 32;
+constexpr int kPairStages = 6;
+constexpr int kPairStage = 2 * 16384;  // per CTA: 128 token rows, 128 weight rows, 128 columns
+constexpr int kPairSfCol = 256;        // scale words behind the accumulators: 4 + 8 columns per slot
+constexpr int kPairGroup = 8;
+
+struct PairParams {
+  CUtensorMap w[2], x;
+  const uint8_t* sw[2];
+  const uint8_t* sx;
+  const float* base;
+  void* out;
+  uint8_t* codes;
+  uint8_t* scales;
+  int* err;
+  int T, N, KB;
+  int m_tiles, n_tiles;
+  int vec32, sf_vec;  // rows aligned to 32 bytes / scale rows to 4
+};
+
+struct PairBars {
+  uint64_t full[kPairStages], empty[kPairStages], sf_full[kSfSlots], sf_empty[kSfSlots], acc_full, acc_empty, done;
+  uint32_t tmem_slot;
+  int abort_flag;
+  uint32_t amax[2][2][128];  // [tile parity][column half][token]
+};
+
+enum PairEpi { kPairBf16 = 0, kPairF32 = 1, kPairGatedBf16 = 2, kPairGatedCodes = 3 };
+
+__device__ __forceinline__ void pair_tile(const PairParams& p, int i, int& mt, int& nt) {
+  const int per = kPairGroup * p.n_tiles, g = i / per, r = i - g * per;
+  const int rows = min(kPairGroup, p.m_tiles - g * kPairGroup);
+  nt = r / rows, mt = g * kPairGroup + r - nt * rows;
+}
+
+__device__ __forceinline__ void store32(void* dst, const uint32_t* v, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_constant__ PairParams p) {
+  constexpr bool kGated = EPI == kPairGatedBf16 || EPI == kPairGatedCodes;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* ring = smem;
+  PairBars& bars = *reinterpret_cast<PairBars*>(smem + kPairStages * kPairStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int n_tiles = p.m_tiles * p.n_tiles, nq = (p.KB + 3) / 4;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) mbar_init(&bars.full[s], 1), mbar_init(&bars.empty[s], 1);
+    for (int s = 0; s < kSfSlots; ++s) mbar_init(&bars.sf_full[s], 8), mbar_init(&bars.sf_empty[s], 1);
+    mbar_init(&bars.acc_full, 1), mbar_init(&bars.acc_empty, 16), mbar_init(&bars.done, 1);
+    bars.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&bars.tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the other CTA's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_slot;
+  volatile int* abort_flag = &bars.abort_flag;
+  pdl_trigger();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = 0;
+      bool ok = true;
+      for (int tile = pair; tile < n_tiles && ok; tile += pairs) {
+        int mt, nt;
+        pair_tile(p, tile, mt, nt);
+        const int tok = mt * 256 + rank * 128, row = kGated ? nt * 128 : nt * 256 + rank * 128;
+        const CUtensorMap* w = &p.w[kGated ? rank : 0];
+        for (int kb = 0; kb < p.KB; ++kb, ++i) {
+          const int s = i % kPairStages;
+          if (i >= kPairStages && !(ok = mbar_wait(&bars.empty[s], (i / kPairStages - 1) & 1, abort_flag, p.err))) break;
+          uint8_t* st = ring + s * kPairStage;
+          // both CTAs' copies complete on the first CTA's barrier
+          if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * kPairStage);
+          const uint32_t full = map_cluster_rank(smem_u32(&bars.full[s]), 0);
+          tma_load_2d_pair(st, &p.x, kb * 128, tok, full);
+          tma_load_2d_pair(st + 16384, w, kb * 128, row, full);
+        }
+      }
+      if (rank == 0) {
+        for (int j = max(0, i - kPairStages); j < i; ++j) mbar_drain(&bars.full[j % kPairStages], (j / kPairStages) & 1);
+      } else if (!ok) {
+        // given up: the copies complete on the other CTA's barrier; leave them time to land
+        for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int i = 0, sq = 0, it = 0;
+      bool ok = true;
+      for (int tile = pair; tile < n_tiles && ok; tile += pairs, ++it) {
+        if (it > 0 && !mbar_wait_cluster(&bars.acc_empty, (it - 1) & 1, abort_flag, p.err)) break;
+        tc_fence_after();
+        for (int kb = 0; kb < p.KB; ++kb, ++i) {
+          const int s = i % kPairStages, slot = sq % kSfSlots;
+          if ((kb & 3) == 0) ok = mbar_wait_cluster(&bars.sf_full[slot], (sq / kSfSlots) & 1, abort_flag, p.err);
+          ok = ok && mbar_wait(&bars.full[s], (i / kPairStages) & 1, abort_flag, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(ring + s * kPairStage);
+          const uint32_t sf = tmem + kPairSfCol + slot * 12;
+          const uint32_t idesc = umma_idesc_mx8(256, 256, kb & 3);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_mx8_pair(tmem, umma_desc_sw128(st + 32 * k), umma_desc_sw128(st + 16384 + 32 * k), idesc, sf, sf + 4,
+                          (kb | k) != 0);
+          umma_commit_pair(&bars.empty[s]);
+          if ((kb & 3) == 3 || kb == p.KB - 1) umma_commit_pair(&bars.sf_empty[slot]), ++sq;
+        }
+        if (ok) umma_commit_pair(&bars.acc_full);
+      }
+      umma_commit_pair(&bars.done);
+    }
+    // the last arrival of a commit on either CTA's barriers
+    if (lane == 0) mbar_drain(&bars.done, 0);
+  } else if (warp < 6) {
+    // scale words of this CTA's tokens (4 columns) and of all 256 weight rows (8 columns)
+    const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
+    const int blocks = (p.N + 127) / 128;
+    int sq = 0;
+    bool ok = true;
+    for (int tile = pair; tile < n_tiles && ok; tile += pairs) {
+      int mt, nt;
+      pair_tile(p, tile, mt, nt);
+      const int tok0 = mt * 256 + rank * 128 + lane;
+      const int b0 = kGated ? nt : 2 * nt, b1 = kGated ? nt : 2 * nt + 1;
+      const uint8_t* w0 = p.sw[0] + int64_t(b0) * p.KB;
+      const uint8_t* w1 = p.sw[kGated ? 1 : 0] + int64_t(b1) * p.KB;
+      for (int q = 0; q < nq; ++q, ++sq) {
+        const int slot = sq % kSfSlots;
+        uint32_t a[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          a[c] = tok0 + 32 * c < p.T ? scale_word(p.sx + int64_t(tok0 + 32 * c) * p.KB, q, p.KB, p.sf_vec) : 0x7f7f7f7fu;
+        const uint32_t u = scale_word(w0, q, p.KB, p.sf_vec);
+        const uint32_t v = b1 < blocks ? scale_word(w1, q, p.KB, p.sf_vec) : 0x7f7f7f7fu;
+        if (sq >= kSfSlots) {
+          ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (sq / kSfSlots - 1) & 1, abort_flag, p.err));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t sf = tmem + quarter + kPairSfCol + slot * 12;
+        tmem_st4(sf, a[0], a[1], a[2], a[3]);
+        tmem_st4(sf + 4, u, u, u, u);
+        tmem_st4(sf + 8, v, v, v, v);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(map_cluster_rank(smem_u32(&bars.sf_full[slot]), 0));
+      }
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 6) >> 2;
+    const int row = quarter * 32 + lane;
+    const uint32_t acc = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t released = map_cluster_rank(smem_u32(&bars.acc_empty), 0);
+    int it = 0;
+    for (int tile = pair; tile < n_tiles; tile += pairs, ++it) {
+      int mt, nt;
+      pair_tile(p, tile, mt, nt);
+      if (!named_bar_and(2, 256, mbar_wait(&bars.acc_full, it & 1, abort_flag, p.err))) break;
+      tc_fence_after();
+      const int64_t tok = int64_t(mt) * 256 + rank * 128 + row;
+      const bool live = tok < p.T;
+      if (EPI == kPairBf16 || EPI == kPairF32) {
+        const int n0 = nt * 256 + half * 128;
+        // bf16: all 128 columns wait packed in registers; fp32: the first half is stored before the
+        // second is loaded
+        uint32_t v[64];
+        for (int part = 0; part < (EPI == kPairF32 ? 2 : 1); ++part) {
+#pragma unroll
+          for (int c = 0; c < (EPI == kPairF32 ? 2 : 4); ++c) {
+            const int col = part * 64 + 32 * c;
+            float f[32];
+            tmem_ld32(acc + half * 128 + col, f);
+            if (p.base && live) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (n0 + col + 4 * j < p.N) {
+                  const float4 b = *reinterpret_cast<const float4*>(p.base + tok * p.N + n0 + col + 4 * j);
+                  f[4 * j] += b.x, f[4 * j + 1] += b.y, f[4 * j + 2] += b.z, f[4 * j + 3] += b.w;
+                }
+            }
+            if (EPI == kPairF32) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[32 * (c & 1) + j] = __float_as_uint(f[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[16 * c + j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+            }
+          }
+          if (EPI == kPairBf16 || part == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(released);
+          }
+          if (live) {
+            constexpr int kElem = EPI == kPairF32 ? 4 : 2;
+            uint8_t* dst = static_cast<uint8_t*>(p.out) + (tok * p.N + n0 + part * 64) * kElem;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int n = n0 + part * 64 + j * (32 / kElem);
+              if (n + 32 / kElem <= p.N) store32(dst + 32 * j, v + 8 * j, p.vec32);
+              else if (n < p.N)  // N is a multiple of 16 bytes
+                *reinterpret_cast<uint4*>(dst + 32 * j) = make_uint4(v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3]);
+            }
+          }
+        }
+      } else {
+        // gate columns half * 64 .. + 63 and the up columns 128 behind them
+        const int f0 = nt * 128 + half * 64;
+        float h[64];
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float g[16], u[16];
+          tmem_ld16x2(acc + half * 64 + 16 * c, acc + 128 + half * 64 + 16 * c, g, u);
+          const bool in = f0 + 16 * c < p.N;  // N is a multiple of 16
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            h[16 * c + j] = silu_mul(g[j], u[j]);
+            m = max(m, in ? mag(h[16 * c + j]) : 0u);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(released);
+        if (EPI == kPairGatedCodes) {
+          // the group's other 64 features are with the thread of the other half
+          bars.amax[it & 1][half][row] = m;
+          asm volatile("bar.sync 3, 256;" ::: "memory");
+          const uint32_t b = scale_byte(max(m, bars.amax[it & 1][half ^ 1][row]));
+          const float inv = scale_inverse(b);
+          if (live) {
+            uint8_t* dst = p.codes + tok * p.N + f0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (f0 + 16 * c >= p.N) continue;
+              const float* x = h + 16 * c;
+              *reinterpret_cast<uint4*>(dst + 16 * c) =
+                  make_uint4(pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                             pack4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv),
+                             pack4(x[8] * inv, x[9] * inv, x[10] * inv, x[11] * inv),
+                             pack4(x[12] * inv, x[13] * inv, x[14] * inv, x[15] * inv));
+            }
+            if (half == 0) p.scales[tok * ((p.N + 127) / 128) + nt] = uint8_t(b);
+          }
+        } else if (live) {
+          uint8_t* dst = static_cast<uint8_t*>(p.out) + (tok * p.N + f0) * 2;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (f0 + 16 * c >= p.N) continue;
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(h[16 * c + 2 * j], h[16 * c + 2 * j + 1]);
+            store32(dst + 32 * c, v, p.vec32);
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  cluster_sync();  // no copy, MMA or arrival of the pair is still on its way to either CTA
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 // ------------------------------------------------------------------ host side
 inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
@@ -307,6 +603,28 @@ int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, 
                                    dim3(splits, 1, 1), smem, s, p));
 }
 
+// The pair kernel where its tiles fill the SMs and rows can be stored in 16-byte pieces.
+bool use_pair(const scion_fp8* L, int T, bool aligned) {
+  return aligned && T > 256;
+}
+
+template <int EPI>
+int launch_pair(const scion_fp8* L, const StreamParams& q, const uint8_t* x, int T, cudaStream_t s) {
+  constexpr bool kGated = EPI == kPairGatedBf16 || EPI == kPairGatedCodes;
+  constexpr int kElem = EPI == kPairF32 ? 4 : 2;
+  PairParams p{};
+  p.w[0] = L->w[0], p.w[1] = L->w[kGated ? 1 : 0];
+  p.sw[0] = q.sw[0], p.sw[1] = q.sw[1], p.sx = q.sx, p.base = q.base, p.out = q.out, p.codes = q.codes;
+  p.scales = q.scales, p.err = q.err, p.T = T, p.N = q.N, p.KB = q.KB, p.sf_vec = q.sf_vec;
+  p.m_tiles = (T + 255) / 256, p.n_tiles = kGated ? (p.N + 127) / 128 : (p.N + 255) / 256;
+  p.vec32 = int64_t(p.N) * kElem % 32 == 0 && !misaligned(p.out, 32);
+  int st = make_tmap_codes(&p.x, x, T, L->desc.k, 128);
+  if (st != SCION_OK) return st;
+  const int64_t tiles = int64_t(p.m_tiles) * p.n_tiles;
+  const int pairs = int(std::min<int64_t>(tiles, L->sms / 2));
+  return status(launch_pdl_cluster(fp8_pair_kernel<EPI>, dim3(2 * pairs), dim3(kPairThreads), dim3(2, 1, 1), kSmem, s, p));
+}
+
 StreamParams params(const scion_fp8* L, const uint8_t* sx, int T) {
   StreamParams p{};
   p.sx = sx, p.sw[0] = L->desc.w_scales, p.sw[1] = L->desc.up_scales;
@@ -342,6 +660,9 @@ extern "C" int scion_fp8_create(const scion_fp8_desc* D, void* stream, scion_fp8
   // (a function attribute of the current device)
   for (const auto f : {scion::fp8_stream_kernel<1>, scion::fp8_stream_kernel<2>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, scion::kSmem);
+  for (const auto f : {scion::fp8_pair_kernel<scion::kPairBf16>, scion::fp8_pair_kernel<scion::kPairF32>,
+                       scion::fp8_pair_kernel<scion::kPairGatedBf16>, scion::fp8_pair_kernel<scion::kPairGatedCodes>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, scion::kSmem);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&L->err), sizeof(int));
   if (e == cudaSuccess) e = cudaMemsetAsync(L->err, 0, sizeof(int), static_cast<cudaStream_t>(stream));
   // (the word is cleared before a forward on another stream can run)
@@ -372,7 +693,12 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
   scion::StreamParams p = scion::params(L, x_scales, T);
   p.base = base, p.out = out, p.out_bf16 = out_type == SCION_BF16;
   p.vec = p.N % 4 == 0 && !scion::misaligned(base, 16) && !scion::misaligned(out, 16);
-  return scion::launch_stream<1>(L, p, x_codes, T, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool rows16 = int64_t(p.N) * (p.out_bf16 ? 2 : 4) % 16 == 0 && p.vec;
+  if (scion::use_pair(L, T, rows16))
+    return p.out_bf16 ? scion::launch_pair<scion::kPairBf16>(L, p, x_codes, T, s)
+                      : scion::launch_pair<scion::kPairF32>(L, p, x_codes, T, s);
+  return scion::launch_stream<1>(L, p, x_codes, T, s);
 }
 
 extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* L,
@@ -385,7 +711,11 @@ extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_
     return SCION_EINVAL;
   scion::StreamParams p = scion::params(L, x_scales, T);
   p.out = h_bf16, p.codes = h_codes, p.scales = h_scales;
-  return scion::launch_stream<2>(L, p, x_codes, T, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (scion::use_pair(L, T, true))
+    return h_codes ? scion::launch_pair<scion::kPairGatedCodes>(L, p, x_codes, T, s)
+                   : scion::launch_pair<scion::kPairGatedBf16>(L, p, x_codes, T, s);
+  return scion::launch_stream<2>(L, p, x_codes, T, s);
 }
 
 extern "C" int scion_fp8_check(const scion_fp8* L, void* stream) {

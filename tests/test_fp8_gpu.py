@@ -208,7 +208,8 @@ class Case:
 
 LINEAR = [(1, 16, 1), (1, 2048, 512), (1, 4096, 2048), (2, 128, 128), (7, 144, 100), (16, 512, 129), (17, 528, 300),
           (33, 2048, 257), (64, 4112, 384), (65, 256, 1000), (100, 2064, 256), (128, 640, 640), (129, 1024, 255),
-          (200, 2048, 1111), (257, 512, 513), (300, 4096, 512), (513, 272, 2048), (1025, 1024, 768)]
+          (200, 2048, 1111), (257, 512, 513), (300, 4096, 512), (513, 272, 2048), (1025, 1024, 768),
+          (300, 640, 264), (400, 144, 260), (700, 16, 136), (2600, 640, 2304)]
 
 
 @pytest.mark.parametrize("T,K,N", LINEAR)
@@ -260,7 +261,7 @@ def test_linear_scale_range(T):
 
 GATED = [(1, 16, 16), (1, 2048, 512), (2, 128, 128), (7, 144, 112), (16, 512, 144), (33, 2048, 272), (50, 2048, 528),
          (64, 4112, 384), (65, 256, 1008), (100, 2064, 256), (129, 1024, 240), (257, 512, 528), (300, 2048, 512),
-         (1025, 1024, 768)]
+         (1025, 1024, 768), (600, 16, 16), (2600, 640, 1040)]
 
 
 def gated_value(g, u, eg, eu):
