@@ -1,7 +1,7 @@
 """Python binding of libscion: the B200 forward pass of one ternary MoE block.
 
-Argument marshalling only: every function here forwards to the C ABI declared in
-``include/scion.h`` (same names), and every step of the block runs in the
+Argument marshalling only (ctypes, and a CPython extension for the calls made once per layer and
+token): every function here forwards to the C ABI declared in ``include/scion.h`` (same names), and every step of the block runs in the
 library's CUDA kernels.  PyTorch supplies device memory and streams.  If the
 library has not been built, the first call raises -- there is no fallback.
 
@@ -470,72 +470,45 @@ def scion_corr_check(corr: Corr, stream=None) -> int:
 
 
 # ------------------------------------------------------- 8-bit dense operators
-# These calls run once per layer and token, so their argument checks are kept to a few attribute
-# reads per tensor: device (the current one), dtype, layout and element count.
-_torch = None
+# These calls run once per layer and token and their kernels take a few microseconds, so the tensor
+# checks (device, dtype, layout, element count) and the call run in the _binding extension.
+_ext = None
 
 
-def _lib_torch():
-    """(the library, torch); torch is imported by the first call."""
-    global _torch
-    if _torch is None:
-        import torch
+def _bind():
+    """The extension, bound to the library's functions by the first call."""
+    global _ext
+    if _ext is None:
+        lib = _load()
+        if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+            raise ImportError("_binding.so is not built (run __graft_entry__.build() or "
+                              "python -m ternary_quantized_moe_b200.build); there is no fallback path")
+        import torch  # noqa: F401  (its libraries are the extension's)
 
-        _torch = torch
-    return _lib or _load(), _torch
+        from . import _binding
 
-
-def _arg(t, name, dtypes, numel, dev):
-    """Device pointer of a contiguous tensor of the given types and element count on device `dev`."""
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous CUDA tensor on the current device" % name)
-    if t.dtype not in dtypes:
-        raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
-    if t.numel() != numel:
-        raise ValueError("%s has %d elements, expected %d" % (name, t.numel(), numel))
-    return t.data_ptr()
-
-
-def _raw_stream(stream, torch, dev):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _code_types(torch):
-    return (torch.float8_e4m3fn, torch.uint8)
-
-
-def _scale_types(torch):
-    return (torch.float8_e8m0fnu, torch.uint8)
-
-
-def _float_type(t, name, torch):
-    if t.dtype == torch.float32:
-        return SCION_F32
-    if t.dtype == torch.bfloat16:
-        return SCION_BF16
-    raise ValueError("%s has dtype %s, expected float32 or bfloat16" % (name, t.dtype))
+        _binding.init(*(C.cast(getattr(lib, n), C.c_void_p).value for n in (
+            "scion_rmsnorm_forward", "scion_fp8_quantize_device", "scion_fp8_forward", "scion_fp8_gated_forward")))
+        _ext = _binding
+    return _ext
 
 
 def scion_fp8_quantize_device(src, codes=None, scales=None, block_rows: int = 1, stream=None):
     """src: fp32 or bf16 CUDA [rows, cols] -> (codes e4m3 [rows, cols], scales E8M0
-    [ceil(rows / block_rows), ceil(cols / 128)]); block_rows 1 (activations) or 128 (weights)."""
-    lib, torch = _lib_torch()
-    if src.dim() != 2:
-        raise ValueError("src must be [rows, cols]")
-    rows, cols = src.shape
-    shape = ((rows + block_rows - 1) // block_rows if block_rows > 0 else 0, (cols + 127) // 128)
-    if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=src.device)
-    if scales is None:
-        scales = torch.empty(shape, dtype=torch.float8_e8m0fnu, device=src.device)
-    dev = torch.cuda.current_device()
-    st = lib.scion_fp8_quantize_device(
-        _float_type(src, "src", torch), _arg(src, "src", (src.dtype,), rows * cols, dev), rows, cols, int(block_rows),
-        _arg(codes, "codes", _code_types(torch), rows * cols, dev),
-        _arg(scales, "scales", _scale_types(torch), shape[0] * shape[1], dev), _raw_stream(stream, torch, dev))
-    _check(st, "scion_fp8_quantize_device")
+    [ceil(rows / block_rows), ceil(cols / 128)]); block_rows 1 (activations) or 128 (weights).
+    Codes may also be uint8 tensors, and scales too, here and below."""
+    if codes is None or scales is None:
+        import torch
+
+        rows, cols = src.shape
+        if codes is None:
+            codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=src.device)
+        if scales is None:
+            shape = (-(-rows // max(block_rows, 1)), (cols + 127) // 128)
+            scales = torch.empty(shape, dtype=torch.float8_e8m0fnu, device=src.device)
+    st = (_ext or _bind()).quantize(src, codes, scales, block_rows, stream)
+    if st:
+        _check(st, "scion_fp8_quantize_device")
     return codes, scales
 
 
@@ -544,26 +517,15 @@ def scion_rmsnorm_forward(x, T: int, weight, eps: float, resid=None, resid_out=N
     """r = x + resid; resid_out = r; y = r / sqrt(mean(r^2) + eps) * weight.  x: fp32 or bf16 CUDA
     [T, d]; resid / resid_out: fp32 or bf16 CUDA [T, d] of one type (optional); weight: bf16 CUDA [d];
     y: bf16 CUDA [T, d]; y_codes / y_scales: e4m3 CUDA [T, d] and E8M0 CUDA [T, ceil(d / 128)]."""
-    lib, torch = _lib_torch()
-    d = weight.numel()
-    dev = torch.cuda.current_device()
-    n = T * d
-    xt = _float_type(x, "x", torch)
-    r = resid if resid is not None else resid_out
-    rt = _float_type(r, "resid", torch) if r is not None else xt
-    st = lib.scion_rmsnorm_forward(
-        _arg(x, "x", (x.dtype,), n, dev), xt, None if resid is None else _arg(resid, "resid", (r.dtype,), n, dev), rt,
-        _arg(weight, "weight", (torch.bfloat16,), d, dev), eps, T, d,
-        None if resid_out is None else _arg(resid_out, "resid_out", (r.dtype,), n, dev),
-        None if y is None else _arg(y, "y", (torch.bfloat16,), n, dev),
-        None if y_codes is None else _arg(y_codes, "y_codes", _code_types(torch), n, dev),
-        None if y_scales is None else _arg(y_scales, "y_scales", _scale_types(torch), T * ((d + 127) // 128), dev),
-        _raw_stream(stream, torch, dev))
-    _check(st, "scion_rmsnorm_forward")
+    st = (_ext or _bind()).rmsnorm(x, T, weight, eps, resid, resid_out, y, y_codes, y_scales, stream)
+    if st:
+        _check(st, "scion_rmsnorm_forward")
 
 
 class Fp8Layer:
     """Owns a scion_fp8 handle; keeps the weights the library reads in place alive."""
+
+    __slots__ = ("handle", "n", "k", "gated", "device", "_keep")
 
     def __init__(self, handle: int, n: int, k: int, gated: bool, device: int, keep):
         self.handle, self.n, self.k, self.gated, self.device, self._keep = handle, n, k, gated, device, keep
@@ -582,76 +544,58 @@ class Fp8Layer:
 def scion_fp8_create(w_codes, w_scales, up_codes=None, up_scales=None, stream=None) -> Fp8Layer:
     """w_codes: e4m3 CUDA [n, k]; w_scales: E8M0 CUDA [ceil(n / 128), ceil(k / 128)]; with up_codes /
     up_scales (same shapes) a gated layer whose gate projection is w."""
-    lib, torch = _lib_torch()
+    import torch
+
     if w_codes.dim() != 2:
         raise ValueError("w_codes must be [n, k]")
     n, k = w_codes.shape
-    ns = ((n + 127) // 128) * ((k + 127) // 128)
     dev = torch.cuda.current_device()
     D = _Fp8Desc()
     D.n, D.k = n, k
-    D.w_codes = _arg(w_codes, "w_codes", _code_types(torch), n * k, dev)
-    D.w_scales = _arg(w_scales, "w_scales", _scale_types(torch), ns, dev)
-    D.up_codes = None if up_codes is None else _arg(up_codes, "up_codes", _code_types(torch), n * k, dev)
-    D.up_scales = None if up_scales is None else _arg(up_scales, "up_scales", _scale_types(torch), ns, dev)
+    codes, scales = (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+    for name, t, types, numel in (("w_codes", w_codes, codes, n * k), ("up_codes", up_codes, codes, n * k),
+                                  ("w_scales", w_scales, scales, -(-n // 128) * -(-k // 128)),
+                                  ("up_scales", up_scales, scales, -(-n // 128) * -(-k // 128))):
+        if t is not None and (t.numel() != numel or t.get_device() != dev):
+            raise ValueError("%s must have %d elements on the current device" % (name, numel))
+        setattr(D, name, _dptr(t, name, types))
     h = C.c_void_p()
-    _check(lib.scion_fp8_create(C.byref(D), _raw_stream(stream, torch, dev), C.byref(h)), "scion_fp8_create")
+    _check(_load().scion_fp8_create(C.byref(D), _stream(stream), C.byref(h)), "scion_fp8_create")
     return Fp8Layer(h.value, n, k, up_codes is not None, dev, (w_codes, w_scales, up_codes, up_scales))
 
 
 def scion_fp8_destroy(layer: Fp8Layer) -> None:
     if layer.handle:
-        _load().scion_fp8_destroy(layer.handle)
+        _load().scion_fp8_destroy(C.c_void_p(layer.handle))
         layer.handle = 0
         layer._keep = None
 
 
 def scion_fp8_device_bytes(layer: Fp8Layer) -> int:
-    return int(_load().scion_fp8_device_bytes(layer.handle))
+    return int(_load().scion_fp8_device_bytes(C.c_void_p(layer.handle)))
 
 
 def scion_fp8_check(layer: Fp8Layer, stream=None) -> int:
     """Waits for the stream and returns (and clears) the layer's device status word."""
-    lib, torch = _lib_torch()
-    return int(lib.scion_fp8_check(layer.handle, _raw_stream(stream, torch, layer.device)))
-
-
-def _fp8_input(x_codes, x_scales, T, layer, torch):
-    """(device, x_codes pointer, x_scales pointer) of a forward's input."""
-    dev = torch.cuda.current_device()
-    if dev != layer.device:
-        raise ValueError("the layer is on device %d, the current device is %d" % (layer.device, dev))
-    k = layer.k
-    return (dev, _arg(x_codes, "x_codes", _code_types(torch), T * k, dev),
-            _arg(x_scales, "x_scales", _scale_types(torch), T * ((k + 127) // 128), dev))
+    return int(_load().scion_fp8_check(C.c_void_p(layer.handle), _stream(stream)))
 
 
 def scion_fp8_forward(x_codes, x_scales, T: int, layer: Fp8Layer, out, base=None, stream=None) -> None:
     """out = base + W x: x_codes e4m3 CUDA [T, k], x_scales E8M0 CUDA [T, ceil(k / 128)]; out fp32 or bf16
     CUDA [T, n]; base fp32 CUDA [T, n] (optional, may be an fp32 out)."""
-    lib, torch = _lib_torch()
-    dev, xp, sp = _fp8_input(x_codes, x_scales, T, layer, torch)
-    n = T * layer.n
-    st = lib.scion_fp8_forward(xp, sp, T, layer.handle,
-                               None if base is None else _arg(base, "base", (torch.float32,), n, dev),
-                               _arg(out, "out", (out.dtype,), n, dev), _float_type(out, "out", torch),
-                               _raw_stream(stream, torch, dev))
-    _check(st, "scion_fp8_forward")
+    st = (_ext or _bind()).forward(x_codes, x_scales, T, layer.handle, layer.n, layer.k, layer.device, out, base, stream)
+    if st:
+        _check(st, "scion_fp8_forward")
 
 
 def scion_fp8_gated_forward(x_codes, x_scales, T: int, layer: Fp8Layer, h=None, h_codes=None, h_scales=None,
                             stream=None) -> None:
     """h = silu(W_gate x) * (W_up x): h bf16 CUDA [T, n], or h_codes e4m3 CUDA [T, n] with h_scales E8M0 CUDA
     [T, ceil(n / 128)]."""
-    lib, torch = _lib_torch()
-    dev, xp, sp = _fp8_input(x_codes, x_scales, T, layer, torch)
-    n = layer.n
-    st = lib.scion_fp8_gated_forward(
-        xp, sp, T, layer.handle, None if h is None else _arg(h, "h", (torch.bfloat16,), T * n, dev),
-        None if h_codes is None else _arg(h_codes, "h_codes", _code_types(torch), T * n, dev),
-        None if h_scales is None else _arg(h_scales, "h_scales", _scale_types(torch), T * ((n + 127) // 128), dev),
-        _raw_stream(stream, torch, dev))
-    _check(st, "scion_fp8_gated_forward")
+    st = (_ext or _bind()).gated(x_codes, x_scales, T, layer.handle, layer.n, layer.k, layer.device, h, h_codes, h_scales,
+                                 stream)
+    if st:
+        _check(st, "scion_fp8_gated_forward")
 
 
 # ------------------------------------------------------------ measurement

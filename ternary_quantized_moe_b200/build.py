@@ -3,7 +3,9 @@
 Each .cu under csrc/ compiles to an object under _build/ (in parallel, skipped when
 up to date), then everything links into ternary_quantized_moe_b200/libscion.so.
 The CUDA runtime is linked statically, so the library loads on machines without a
-GPU (every call then reports SCION_ECUDA).
+GPU (every call then reports SCION_ECUDA).  csrc/binding.cpp, the CPython extension of
+the per-token calls, compiles with the host compiler against torch's headers into
+ternary_quantized_moe_b200/_binding.so.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libscion.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
@@ -49,11 +53,31 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    src = os.path.join(CSRC, "binding.cpp")
+    if not _stale(BINDING, [src, os.path.join(ROOT, "include", "scion.h")]):
+        return
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    inc = include_paths() + [cuda, sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    subprocess.check_call([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+                           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+                          + ["-isystem" + i for i in inc] + [src, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib,
+                             "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with ThreadPoolExecutor(max_workers=min(8, len(sources))) as ex:
+    with ThreadPoolExecutor(max_workers=min(9, len(sources) + 1)) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, sources))
+        binding.result()
     if _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         subprocess.check_call([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"])
