@@ -29,10 +29,14 @@ typedef __nv_bfloat16 bf16;
 // ------------------------------------------------------------------ streaming kernel
 // Few tokens: bound by reading the weights once.  The weights are the M side (128 rows per tile),
 // the tokens the N side (bn of them, a multiple of 16), and the CTAs of a cluster split K, so that a
-// matrix of few tiles still spreads over the SMs; their partial sums meet in distributed shared
-// memory and are added in rank order.  Roles: warp 0 TMA loads through a ring of 128-column stages,
-// warp 1 the MMAs, warps 2..5 the scale words (global -> tensor memory) and the epilogue.
-constexpr int kStreamThreads = 192;
+// matrix of few tiles still spreads over the SMs.  Partial sums: the tokens of a tile are dealt to
+// the CTAs of the cluster in groups of four; every CTA stores its sums of a group straight into the
+// shared memory of the group's owner (every warp then arrives on a barrier there), and the owner
+// adds them in rank order.  One barrier of the cluster, at the start, and none on the way out: an
+// owner leaves when everything sent to it has arrived.
+// Roles: warp 0 TMA loads through a ring of 128-column stages, warp 1 the MMAs, warps 2..9 the
+// epilogue (two per lane quarter, alternate 16-token chunks), warps 2..5 also the scale words.
+constexpr int kStreamThreads = 320;
 constexpr int kMaxStages = 12;
 constexpr int kSfSlots = 4;  // ring of scale words, each slot for 4 K blocks (one byte each)
 constexpr uint32_t kSmem = 227 * 1024;
@@ -52,9 +56,10 @@ struct StreamParams {
 };
 
 struct Bars {
-  uint64_t full[kMaxStages], empty[kMaxStages], sf_full[kSfSlots], sf_empty[kSfSlots], acc_full, done;
+  uint64_t full[kMaxStages], empty[kMaxStages], sf_full[kSfSlots], sf_empty[kSfSlots], acc_full, done, sums;
   uint32_t tmem_slot;
   int abort_flag;
+  uint32_t amax[2][2][16][4];  // [thread group][parity][token][lane quarter]
 };
 
 // Scale bytes of K blocks 4q .. 4q + 3 of one row; blocks past the end read as 2^0.
@@ -67,16 +72,63 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int q, int KB
   return w;
 }
 
-__device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+// Four floats into the shared memory of another CTA of the cluster (or this one).
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
+// The results of one feature (of the 128 a group of four warps holds) for NT tokens from t on.
+// `live`: tokens t .. t + live - 1 exist.  All 128 threads of the group take part.
+template <int NW, int NT>
+__device__ __forceinline__ void stream_store(const StreamParams& p, Bars& bars, const float (&a)[NT], const float (&b)[NT],
+                                             int64_t t, int live, int group, int& parity) {
+  const int quarter = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int n = blockIdx.y * 128 + quarter * 32 + lane;
+  const bool in = n < p.N;
+  const int64_t at = t * p.N + n;
+  if (NW == 1) {
+    if (!in) return;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (i >= live) break;
+      const int64_t o = at + int64_t(i) * p.N;
+      const float v = p.base ? p.base[o] + a[i] : a[i];
+      if (p.out_bf16) static_cast<bf16*>(p.out)[o] = __float2bfloat16_rn(v);
+      else static_cast<float*>(p.out)[o] = v;
+    }
+    return;
+  }
+  float h[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) h[i] = silu_mul(a[i], b[i]);
+  if (p.codes) {
+    // the largest magnitude over the 128 features: within the warps, then over the four of them
+    uint32_t(*amax)[4] = bars.amax[group][parity];
+    parity ^= 1;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, in ? mag(h[i]) : 0u);
+      if (lane == i) amax[i][quarter] = m;
+    }
+    asm volatile("bar.sync %0, 128;" ::"r"(4 + group) : "memory");
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (i >= live) break;
+      const uint4 m = *reinterpret_cast<const uint4*>(amax[i]);
+      const uint32_t s = scale_byte(max(max(m.x, m.y), max(m.z, m.w)));
+      if (in) p.codes[at + int64_t(i) * p.N] = uint8_t(pack4(h[i] * scale_inverse(s), 0.f, 0.f, 0.f));
+      if (quarter == 0 && lane == 0) p.scales[(t + i) * ((p.N + 127) / 128) + blockIdx.y] = uint8_t(s);
+    }
+  } else if (in) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (i >= live) break;
+      static_cast<bf16*>(p.out)[at + int64_t(i) * p.N] = __float2bfloat16_rn(h[i]);
+    }
+  }
+}
 
 // NW = 1: out = base + W x.  NW = 2: h = silu(W0 x) (W1 x), to bf16 or codes and scales.
 template <int NW>
@@ -84,29 +136,38 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars& bars = *reinterpret_cast<Bars*>(smem);
-  uint8_t* ring = smem + 1024;
+  uint8_t* ring = smem + 2048;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x, splits = gridDim.x;
   const int row0 = blockIdx.y * 128, tok0 = blockIdx.z * p.bn;
   const int kb0 = int(int64_t(rank) * p.KB / splits), kb1 = int(int64_t(rank + 1) * p.KB / splits);
   const uint32_t stage_bytes = NW * 16384 + p.bn * 128;
+  const int nt = min(p.bn, p.T - tok0), quads = (nt + 3) / 4;
+  // this CTA's groups of four tokens and what arrives for them: [group][sender][matrix][feature][4]
+  const int mine = rank < quads ? (quads - rank + splits - 1) / splits : 0;
+  const uint32_t sums = smem_u32(ring + p.stages * stage_bytes);
 
   if (threadIdx.x == 0) {
+    tma_prefetch_map(&p.w[0]), tma_prefetch_map(&p.x);
+    if (NW == 2) tma_prefetch_map(&p.w[1]);
     for (int s = 0; s < p.stages; ++s) mbar_init(&bars.full[s], 1), mbar_init(&bars.empty[s], 1);
     for (int s = 0; s < kSfSlots; ++s) mbar_init(&bars.sf_full[s], 128), mbar_init(&bars.sf_empty[s], 1);
-    mbar_init(&bars.acc_full, 1), mbar_init(&bars.done, 1);
+    mbar_init(&bars.acc_full, 1), mbar_init(&bars.done, 1), mbar_init(&bars.sums, 8 * splits);
     bars.abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&bars.tmem_slot, p.tmem_cols);
   tc_fence_before();
   __syncthreads();
+  // the barriers of the cluster exist before anything is sent (awaited before the first store)
+  if (splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = bars.tmem_slot;
   volatile int* abort_flag = &bars.abort_flag;
   pdl_trigger();
   pdl_wait();
 
+  bool joined = splits == 1;
   if (warp == 0) {
     if (lane == 0) {
       int i = 0;
@@ -147,114 +208,105 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
         if ((kb & 3) == 3) umma_commit(&bars.sf_empty[slot]);
       }
       if (ok) umma_commit(&bars.acc_full);
-      // every MMA issued above has finished before shared and tensor memory are reused
+      // every MMA issued above has finished before tensor memory is released
       umma_commit(&bars.done);
       mbar_drain(&bars.done, 0);
     }
   } else {
-    // scale words: each of the four warps writes them to its own lane quarter
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
-    const int q0 = kb0 / 4, nq = (kb1 - 1) / 4 - q0 + 1;
+    const int group = (warp - 2) >> 2;
     bool ok = true;
-    for (int i = 0; i < nq; ++i) {
-      const int slot = i % kSfSlots, q = q0 + i;
-      uint32_t wa[NW], wb[8];
+    if (group == 0) {
+      // scale words: each of the four warps writes them to its own lane quarter
+      const int q0 = kb0 / 4, nq = (kb1 - 1) / 4 - q0 + 1;
+      for (int i = 0; i < nq; ++i) {
+        const int slot = i % kSfSlots, q = q0 + i;
+        uint32_t wa[NW], wb[8];
 #pragma unroll
-      for (int m = 0; m < NW; ++m) wa[m] = scale_word(p.sw[m] + int64_t(blockIdx.y) * p.KB, q, p.KB, p.sf_vec);
+        for (int m = 0; m < NW; ++m) wa[m] = scale_word(p.sw[m] + int64_t(blockIdx.y) * p.KB, q, p.KB, p.sf_vec);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int t = tok0 + 32 * c + lane;
-        wb[c] = 32 * c < p.bn && t < p.T ? scale_word(p.sx + int64_t(t) * p.KB, q, p.KB, p.sf_vec) : 0x7f7f7f7fu;
+        for (int c = 0; c < 8; ++c) {
+          const int t = tok0 + 32 * c + lane;
+          wb[c] = 32 * c < p.bn && t < p.T ? scale_word(p.sx + int64_t(t) * p.KB, q, p.KB, p.sf_vec) : 0x7f7f7f7fu;
+        }
+        if (i >= kSfSlots) {
+          ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (i / kSfSlots - 1) & 1, abort_flag, p.err));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t sf = tmem + quarter + p.sf_col + slot * (4 * NW + p.sfb_cols);
+#pragma unroll
+        for (int m = 0; m < NW; ++m) tmem_st4(sf + 4 * m, wa[m], wa[m], wa[m], wa[m]);
+        tmem_st4(sf + 4 * NW, wb[0], wb[1], wb[2], wb[3]);
+        if (p.sfb_cols > 4) tmem_st4(sf + 4 * NW + 4, wb[4], wb[5], wb[6], wb[7]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars.sf_full[slot]);
       }
-      if (i >= kSfSlots) {
-        ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (i / kSfSlots - 1) & 1, abort_flag, p.err));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const uint32_t sf = tmem + quarter + p.sf_col + slot * (4 * NW + p.sfb_cols);
-#pragma unroll
-      for (int m = 0; m < NW; ++m) tmem_st4(sf + 4 * m, wa[m], wa[m], wa[m], wa[m]);
-      tmem_st4(sf + 4 * NW, wb[0], wb[1], wb[2], wb[3]);
-      if (p.sfb_cols > 4) tmem_st4(sf + 4 * NW + 4, wb[4], wb[5], wb[6], wb[7]);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars.sf_full[slot]);
     }
-    // partial sums to shared memory [matrix][token][128 features] (the ring is free: every load has
-    // been read by an MMA, and every MMA has finished)
-    if (ok && named_bar_and(1, 128, mbar_wait(&bars.acc_full, 0, abort_flag, p.err))) {
+    ok = named_bar_and(2, 256, ok && mbar_wait(&bars.acc_full, 0, abort_flag, p.err));
+    if (splits > 1) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      joined = true;
+    }
+    int parity = 0;
+    if (ok) {
       tc_fence_after();
-      float* part = reinterpret_cast<float*>(ring) + (warp & 3) * 32 + lane;
-      for (int c = 0; c < NW * p.bn; c += 16) {
-        float v[16];
-        tmem_ld16(tmem + quarter + c, v);
+      const uint32_t feature = (warp & 3) * 32 + lane;
+      for (int c = 16 * group; c < nt; c += 32) {
+        float v[16], u[16];
+        if (NW == 2) tmem_ld16x2(tmem + quarter + c, tmem + quarter + p.bn + c, v, u);
+        else tmem_ld16(tmem + quarter + c, v);
+        if (splits == 1) {
+          stream_store<NW, 16>(p, bars, v, u, tok0 + c, nt - c, group, parity);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * 128] = v[i];
+          for (int i = 0; i < 4; ++i) {
+            const int q = c / 4 + i;
+            if (q >= quads) break;
+            const uint32_t owner = q % splits;
+            const uint32_t dst = map_cluster_rank(sums, owner) + ((q / splits) * splits + rank) * (NW * 2048) + feature * 16;
+            st_cluster_f4(dst, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (NW == 2) st_cluster_f4(dst + 2048, u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+          }
+        }
       }
-      tc_fence_before();
+      __syncwarp();
+      if (splits > 1 && lane < min(splits, quads)) mbar_arrive_remote(map_cluster_rank(smem_u32(&bars.sums), lane));
     }
+    if (splits > 1 && mine > 0) {
+      // (an aborted CTA sends nothing: its owners' waits run out, and the status word says so)
+      if (named_bar_and(2, 256, mbar_wait_cluster(&bars.sums, 0, abort_flag, p.err))) {
+        for (int j = group; j < mine; j += 2) {
+          const uint32_t at = sums + j * splits * (NW * 2048) + ((warp & 3) * 32 + lane) * 16;
+          float v[4] = {}, u[4] = {};
+          for (int r = 0; r < splits; ++r) {
+            const float4 a = lds_f4(at + r * (NW * 2048));
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+            if (NW == 2) {
+              const float4 b = lds_f4(at + r * (NW * 2048) + 2048);
+              u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
+            }
+          }
+          const int t = 4 * (rank + j * splits);
+          stream_store<NW, 4>(p, bars, v, u, tok0 + t, nt - t, group, parity);
+        }
+      }
+    }
+    tc_fence_before();
   }
+  __syncwarp();
+  if (!joined) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
-  if (splits > 1) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
   }
-
-  // tokens rank, rank + splits, ... of the tile: a warp per token, 4 features per lane
-  const int nt = min(p.bn, p.T - tok0);
-  const int n = row0 + 4 * lane;
-  const uint32_t mine = smem_u32(ring) + 16 * lane;
-  for (int t = rank + splits * warp; t < nt; t += splits * (kStreamThreads / 32)) {
-    float v[NW][4];
-#pragma unroll
-    for (int m = 0; m < NW; ++m) {
-      const uint32_t at = mine + uint32_t(m * p.bn + t) * 512;
-      float4 s = ld_dsmem_f4(map_cluster_rank(at, 0));
-      for (int r = 1; r < splits; ++r) {
-        const float4 o = ld_dsmem_f4(map_cluster_rank(at, r));
-        s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
-      }
-      v[m][0] = s.x, v[m][1] = s.y, v[m][2] = s.z, v[m][3] = s.w;
-    }
-    const int64_t tok = tok0 + t, at = tok * p.N + n;
-    if (NW == 1) {
-      if (p.vec && n < p.N) {  // N a multiple of 4, rows aligned: all four or none
-        if (p.base) {
-          const float4 b = *reinterpret_cast<const float4*>(p.base + at);
-          v[0][0] += b.x, v[0][1] += b.y, v[0][2] += b.z, v[0][3] += b.w;
-        }
-        if (p.out_bf16)
-          *reinterpret_cast<uint2*>(static_cast<bf16*>(p.out) + at) =
-              make_uint2(pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]));
-        else
-          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (n + j >= p.N) continue;
-          const float o = (p.base ? p.base[at + j] : 0.f) + v[0][j];
-          if (p.out_bf16) static_cast<bf16*>(p.out)[at + j] = __float2bfloat16_rn(o);
-          else static_cast<float*>(p.out)[at + j] = o;
-        }
-      }
-    } else {
-      float h[4];
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = silu_mul(v[0][j], v[NW - 1][j]), m = max(m, n < p.N ? mag(h[j]) : 0u);
-      if (p.codes) {
-        const uint32_t b = scale_byte(__reduce_max_sync(0xffffffffu, m));
-        const float inv = scale_inverse(b);
-        if (n < p.N) *reinterpret_cast<uint32_t*>(p.codes + at) = pack4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
-        if (lane == 0) p.scales[tok * ((p.N + 127) / 128) + blockIdx.y] = uint8_t(b);
-      } else if (n < p.N) {
-        *reinterpret_cast<uint2*>(static_cast<bf16*>(p.out) + at) =
-            make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
-      }
-    }
+  if (splits > 1) {
+    // an owner that gave up stays until nothing more can be sent to it; the others need not wait
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (*abort_flag) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
-  if (splits > 1) cluster_sync();  // the other CTAs may still be reading this one's sums
 }
 
 // ------------------------------------------------------------------ pair kernel
@@ -326,6 +378,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   const int n_tiles = p.m_tiles * p.n_tiles, nq = (p.KB + 3) / 4;
 
   if (threadIdx.x == 0) {
+    tma_prefetch_map(&p.w[kGated ? rank : 0]), tma_prefetch_map(&p.x);
     for (int s = 0; s < kPairStages; ++s) mbar_init(&bars.full[s], 1), mbar_init(&bars.empty[s], 1);
     for (int s = 0; s < kSfSlots; ++s) mbar_init(&bars.sf_full[s], 8), mbar_init(&bars.sf_empty[s], 1);
     mbar_init(&bars.acc_full, 1), mbar_init(&bars.acc_empty, 16), mbar_init(&bars.done, 1);
@@ -577,25 +630,30 @@ int status(cudaError_t e) {
 template <int NW>
 int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, cudaStream_t s) {
   p.w[0] = L->w[0], p.w[1] = L->w[NW - 1];
-  // tokens of a tile: the accumulators (NW bn columns) and the scale words share 512 columns
-  const int most = NW == 1 ? 256 : 208;
+  const int n_tiles = (p.N + 127) / 128;
+  // tokens of a tile: the accumulators (NW bn columns) and the scale words share 512 columns of
+  // tensor memory; narrower tiles where the widest would leave SMs without one
+  int most = NW == 1 ? 256 : 208;
+  while (most > 64 && n_tiles * ((T + most - 1) / most) < L->sms / 2) most = most > 128 ? 128 : 64;
   const int t_tiles = (T + most - 1) / most;
   p.bn = ((T + t_tiles - 1) / t_tiles + 15) / 16 * 16;
-  const int n_tiles = (p.N + 127) / 128;
-  const int splits = std::max(1, std::min({8, p.KB, L->sms / (n_tiles * t_tiles)}));
+  const int ctas = n_tiles * t_tiles;
+  // (the sums of a wide tile would leave too little shared memory for the ring)
+  const int splits = p.bn > 128 / NW ? 1 : std::max(1, std::min({8, p.KB, L->sms / ctas}));
   p.sfb_cols = p.bn > 128 ? 8 : 4;
-  p.sf_col = (NW * p.bn + 3) / 4 * 4;
+  p.sf_col = NW * p.bn;
   p.tmem_cols = int(tmem_cols_pow2(p.sf_col + kSfSlots * (4 * NW + p.sfb_cols)));
   // Shared memory in step with tensor memory: CTAs that fit an SM together by the one then fit by
   // the other too, so no CTA of a cluster can wait for tensor memory held by a CTA that waits for
   // its own cluster.
   const uint32_t share = 228 * 1024 / 512 * p.tmem_cols - 1024;
   const uint32_t stage = NW * 16384 + p.bn * 128;
-  const uint32_t budget = std::max<uint32_t>(share, 113 * 1024);
-  p.stages = std::min<int>({kMaxStages, int((budget - 2048) / stage), (p.KB + splits - 1) / splits});
-  p.stages = std::max(p.stages, 1);
-  const uint32_t need = 2048 + std::max<uint32_t>(p.stages * stage, NW * p.bn * 512);
-  const uint32_t smem = std::max(need, share);
+  const int quads = (p.bn + 3) / 4;
+  const uint32_t fixed = 3072 + (splits > 1 ? (quads + splits - 1) / splits * splits * NW * 2048 : 0);
+  // two CTAs per SM where there are more than SMs
+  const uint32_t budget = ctas * splits > L->sms ? std::max<uint32_t>(share, 113 * 1024) : kSmem;
+  p.stages = std::max(1, std::min({kMaxStages, int((budget - fixed) / stage), (p.KB + splits - 1) / splits}));
+  const uint32_t smem = std::max(fixed + p.stages * stage, share);
   if (smem > kSmem) return SCION_EINVAL;
   int st = make_tmap_codes(&p.x, x, T, L->desc.k, p.bn);
   if (st != SCION_OK) return st;
@@ -704,8 +762,8 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
 extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* L,
                                        void* h_bf16, uint8_t* h_codes, uint8_t* h_scales, void* stream) {
   if (!L || !L->desc.up_codes || T < 0) return SCION_EINVAL;
+  if (T == 0) return SCION_OK;  // (empty tensors have null addresses)
   if (!h_codes != !h_scales || !h_codes == !h_bf16) return SCION_EINVAL;
-  if (T == 0) return SCION_OK;
   if (!x_codes || !x_scales || scion::misaligned(x_codes, 16) || scion::misaligned(h_bf16, 16) ||
       scion::misaligned(h_codes, 16))
     return SCION_EINVAL;

@@ -221,8 +221,8 @@ extern "C" int scion_rmsnorm_forward(const void* x, int x_type, const void* resi
   if ((x_type != SCION_F32 && x_type != SCION_BF16) || (resid_type != SCION_F32 && resid_type != SCION_BF16))
     return SCION_EINVAL;
   if (T < 0 || d < 16 || d % 16 || d > 32768 || !(eps >= 0.f) || !isfinite(eps)) return SCION_EINVAL;
+  if (T == 0) return SCION_OK;  // (empty tensors have null addresses)
   if (!y_codes != !y_scales || (!resid_out && !y_bf16 && !y_codes)) return SCION_EINVAL;
-  if (T == 0) return SCION_OK;
   if (!x || !weight) return SCION_EINVAL;
   for (const void* p : {x, resid, weight, static_cast<const void*>(resid_out), static_cast<const void*>(y_bf16),
                         static_cast<const void*>(y_codes)})

@@ -387,8 +387,18 @@ def test_python_refusals():
         with pytest.raises(tq.ScionError) as e:
             f()
         assert e.value.status == tq.SCION_EINVAL
-    empty = torch.empty((0, 256), dtype=torch.uint8, device=DEV)
-    tq.scion_fp8_forward(empty, torch.empty((0, 2), dtype=torch.uint8, device=DEV), 0, c.layer, out[:0])
+
+
+def test_empty_batches():
+    c, g = Case(4, 256, 128), Case(4, 256, 128, gated=True)
+    none = lambda n, t: torch.empty((0, n), dtype=t, device=DEV)  # noqa: E731
+    x, s = none(256, torch.uint8), none(2, torch.uint8)
+    tq.scion_fp8_forward(x, s, 0, c.layer, none(128, F32))
+    tq.scion_fp8_gated_forward(x, s, 0, g.layer, h=none(128, BF16))
+    tq.scion_fp8_gated_forward(x, s, 0, g.layer, h_codes=none(128, torch.uint8), h_scales=none(1, torch.uint8))
+    tq.scion_rmsnorm_forward(none(256, F32), 0, torch.ones(256, dtype=BF16, device=DEV), 1e-6, y=none(256, BF16))
+    codes, scales = tq.scion_fp8_quantize_device(none(256, F32))
+    assert codes.shape == (0, 256) and scales.shape == (0, 2)
 
 
 @pytest.mark.parametrize("T", [3, 200])

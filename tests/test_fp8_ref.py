@@ -99,3 +99,4 @@ def test_null_handles():
 def test_empty_batches_launch_nothing():
     assert quant(rows=0, src=None, codes=None, scales=None) == tq.SCION_OK
     assert norm(T=0, x=None, r=None) == tq.SCION_OK
+    assert norm(T=0, x=None, r=None, ro=None, y=None, c=None, s=None) == tq.SCION_OK
