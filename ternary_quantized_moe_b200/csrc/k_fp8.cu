@@ -39,6 +39,7 @@ typedef __nv_bfloat16 bf16;
 constexpr int kStreamThreads = 320;
 constexpr int kMaxStages = 12;
 constexpr int kSfSlots = 4;  // ring of scale words, each slot for 4 K blocks (one byte each)
+constexpr uint32_t kNoScale = 0x7f7f7f7fu;  // words of rows past the end: 2^0
 constexpr uint32_t kSmem = 227 * 1024;
 
 struct StreamParams {
@@ -52,7 +53,7 @@ struct StreamParams {
   int* err;
   int T, N, KB;
   int bn, stages, tmem_cols, sf_col, sfb_cols;
-  int out_bf16, vec, sf_vec;
+  int out_bf16, vec, sf_align;
 };
 
 struct Bars {
@@ -62,15 +63,37 @@ struct Bars {
   uint32_t amax[2][2][16][4];  // [thread group][parity][token][lane quarter]
 };
 
-// Scale bytes of K blocks 4q .. 4q + 3 of one row; blocks past the end read as 2^0.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int q, int KB, bool vec) {
-  if (vec) return *reinterpret_cast<const uint32_t*>(row + 4 * q);
-  uint32_t w = 0x7f7f7f7fu;
+// Scale bytes of one row are read 16 K blocks at a time (a "round": four words of four blocks), so
+// that the loads of a round overlap and the next round's are in flight while the MMAs use this one;
+// blocks past the end read as 2^0.  `align`: 16-, 4- or 1-byte loads (alignment of the row starts).
+__device__ __forceinline__ uint4 scale_round(const uint8_t* row, int r, int KB, int align) {
+  if (align == 16) return *reinterpret_cast<const uint4*>(row + 16 * r);
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (4 * q + i < KB) w = (w & ~(0xffu << (8 * i))) | (uint32_t(row[4 * q + i]) << (8 * i));
-  return w;
+  for (int i = 0; i < 4; ++i) {
+    const int kb = 16 * r + 4 * i;
+    w[i] = 0x7f7f7f7fu;
+    if (align == 4) {
+      if (kb < KB) w[i] = *reinterpret_cast<const uint32_t*>(row + kb);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (kb + j < KB) w[i] = (w[i] & ~(0xffu << (8 * j))) | (uint32_t(row[kb + j]) << (8 * j));
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// Position in a ring of barriers: slot and the parity of its current phase.  (One thread runs each
+// loop over K, so every instruction of its iteration counts: no divisions by the ring's size.)
+struct RingPos {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int size) {
+    if (++slot == size) slot = 0, parity ^= 1;
+  }
+};
 
 // Four floats into the shared memory of another CTA of the cluster (or this one).
 __device__ __forceinline__ void st_cluster_f4(uint32_t addr, float a, float b, float c, float d) {
@@ -168,80 +191,102 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
   pdl_wait();
 
   bool joined = splits == 1;
+  // the loops over K of warps 0 and 1 are run by the whole warp, with one lane issuing
+  const uint32_t issue = lane == 0;
   if (warp == 0) {
-    if (lane == 0) {
-      int i = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++i) {
-        const int s = i % p.stages;
-        if (i >= p.stages && !mbar_wait(&bars.empty[s], (i / p.stages - 1) & 1, abort_flag, p.err)) break;
-        uint8_t* st = ring + s * stage_bytes;
-        mbar_arrive_expect_tx(&bars.full[s], stage_bytes);
-        tma_load_2d(st, &p.w[0], kb * 128, row0, &bars.full[s]);
-        if (NW == 2) tma_load_2d(st + 16384, &p.w[1], kb * 128, row0, &bars.full[s]);
-        tma_load_2d(st + NW * 16384, &p.x, kb * 128, tok0, &bars.full[s]);
-      }
-      // copies may still be in flight if the MMA warp gave up
-      for (int j = max(0, i - p.stages); j < i; ++j) mbar_drain(&bars.full[j % p.stages], (j / p.stages) & 1);
+    RingPos at;
+    int i = 0;
+    const uint32_t ring0 = smem_u32(ring);
+    uint32_t st = ring0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb, ++i) {
+      if (i >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[at.slot], at.parity ^ 1, abort_flag, p.err));
+      if (!ok) break;
+      uint64_t* full = &bars.full[at.slot];
+      mbar_expect_if(issue, full, stage_bytes);
+      tma_load_2d_if(issue, st, &p.w[0], kb * 128, row0, full);
+      if (NW == 2) tma_load_2d_if(issue, st + 16384, &p.w[1], kb * 128, row0, full);
+      tma_load_2d_if(issue, st + NW * 16384, &p.x, kb * 128, tok0, full);
+      at.next(p.stages);
+      st = at.slot ? st + stage_bytes : ring0;
     }
+    // copies may still be in flight if the MMA warp gave up
+    for (int j = max(0, i - p.stages); j < i; ++j) mbar_drain(&bars.full[j % p.stages], (j / p.stages) & 1);
   } else if (warp == 1) {
-    if (lane == 0) {
-      int i = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1 && ok; ++kb, ++i) {
-        const int s = i % p.stages, q = kb / 4 - kb0 / 4, slot = q % kSfSlots;
-        if (kb == kb0 || (kb & 3) == 0) ok = mbar_wait(&bars.sf_full[slot], (q / kSfSlots) & 1, abort_flag, p.err);
-        ok = ok && mbar_wait(&bars.full[s], (i / p.stages) & 1, abort_flag, p.err);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t st = smem_u32(ring + s * stage_bytes);
-        const uint32_t sf = tmem + p.sf_col + slot * (4 * NW + p.sfb_cols);
-        const uint32_t idesc = umma_idesc_mx8(128, p.bn, kb & 3);
+    RingPos at;
+    bool ok = true;
+    const uint32_t low0 = umma_desc_low(smem_u32(ring));
+    uint32_t low = low0, accumulate = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int slot = (kb >> 2) % kSfSlots;
+      if (kb == kb0 || (kb & 3) == 0)  // (a slot's phase turns over every four words)
+        ok = mbar_wait(&bars.sf_full[slot], ((kb >> 2) - (kb0 >> 2)) / kSfSlots & 1, abort_flag, p.err);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sf = tmem + p.sf_col + slot * (4 * NW + p.sfb_cols);
+      const uint32_t idesc = umma_idesc_mx8(128, p.bn, kb & 3);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t db = umma_desc_sw128(st + NW * 16384 + 32 * k);
+      for (int k = 0; k < 4; ++k) {
 #pragma unroll
-          for (int m = 0; m < NW; ++m)
-            umma_mx8(tmem + m * p.bn, umma_desc_sw128(st + m * 16384 + 32 * k), db, idesc, sf + 4 * m, sf + 4 * NW,
-                     (i | k) != 0);
-        }
-        umma_commit(&bars.empty[s]);
-        if ((kb & 3) == 3) umma_commit(&bars.sf_empty[slot]);
+        for (int m = 0; m < NW; ++m)
+          umma_mx8(issue, tmem + m * p.bn, umma_desc_of(low + m * 1024 + 2 * k), umma_desc_of(low + NW * 1024 + 2 * k),
+                   idesc, sf + 4 * m, sf + 4 * NW, k ? 1 : accumulate);
       }
-      if (ok) umma_commit(&bars.acc_full);
-      // every MMA issued above has finished before tensor memory is released
-      umma_commit(&bars.done);
-      mbar_drain(&bars.done, 0);
+      accumulate = 1;
+      umma_commit_if(issue, &bars.empty[at.slot]);
+      if ((kb & 3) == 3) umma_commit_if(issue, &bars.sf_empty[slot]);
+      at.next(p.stages);
+      low = at.slot ? low + (stage_bytes >> 4) : low0;
     }
+    if (ok) umma_commit_if(issue, &bars.acc_full);
+    // every MMA issued above has finished before tensor memory is released
+    umma_commit_if(issue, &bars.done);
+    mbar_drain(&bars.done, 0);
   } else {
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
     const int group = (warp - 2) >> 2;
     bool ok = true;
     if (group == 0) {
       // scale words: each of the four warps writes them to its own lane quarter
-      const int q0 = kb0 / 4, nq = (kb1 - 1) / 4 - q0 + 1;
-      for (int i = 0; i < nq; ++i) {
-        const int slot = i % kSfSlots, q = q0 + i;
-        uint32_t wa[NW], wb[8];
+      const int q0 = kb0 / 4, q1 = (kb1 - 1) / 4;
+      const int cols = (p.bn + 31) / 32;
+      uint4 wa[NW], wb[8];
+      auto load = [&](int r) {
 #pragma unroll
-        for (int m = 0; m < NW; ++m) wa[m] = scale_word(p.sw[m] + int64_t(blockIdx.y) * p.KB, q, p.KB, p.sf_vec);
+        for (int m = 0; m < NW; ++m) wa[m] = scale_round(p.sw[m] + int64_t(blockIdx.y) * p.KB, r, p.KB, p.sf_align);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const int t = tok0 + 32 * c + lane;
-          wb[c] = 32 * c < p.bn && t < p.T ? scale_word(p.sx + int64_t(t) * p.KB, q, p.KB, p.sf_vec) : 0x7f7f7f7fu;
+          wb[c] = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
+          if (c < cols && t < p.T) wb[c] = scale_round(p.sx + int64_t(t) * p.KB, r, p.KB, p.sf_align);
         }
-        if (i >= kSfSlots) {
-          ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (i / kSfSlots - 1) & 1, abort_flag, p.err));
-          if (!ok) break;
-          tc_fence_after();
-        }
-        const uint32_t sf = tmem + quarter + p.sf_col + slot * (4 * NW + p.sfb_cols);
+      };
+      load(q0 / 4);
+      for (int r = q0 / 4; r <= q1 / 4 && ok; ++r) {
 #pragma unroll
-        for (int m = 0; m < NW; ++m) tmem_st4(sf + 4 * m, wa[m], wa[m], wa[m], wa[m]);
-        tmem_st4(sf + 4 * NW, wb[0], wb[1], wb[2], wb[3]);
-        if (p.sfb_cols > 4) tmem_st4(sf + 4 * NW + 4, wb[4], wb[5], wb[6], wb[7]);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars.sf_full[slot]);
+        for (int slot = 0; slot < kSfSlots; ++slot) {
+          const int q = 4 * r + slot, i = q - q0;
+          if (i < 0 || q > q1) continue;
+          if (i >= kSfSlots) {
+            ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (i / kSfSlots - 1) & 1, abort_flag, p.err));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          const uint32_t sf = tmem + quarter + p.sf_col + slot * (4 * NW + p.sfb_cols);
+#pragma unroll
+          for (int m = 0; m < NW; ++m) {
+            const uint32_t w = word(wa[m], slot);
+            tmem_st4(sf + 4 * m, w, w, w, w);
+          }
+          tmem_st4(sf + 4 * NW, word(wb[0], slot), word(wb[1], slot), word(wb[2], slot), word(wb[3], slot));
+          if (p.sfb_cols > 4)
+            tmem_st4(sf + 4 * NW + 4, word(wb[4], slot), word(wb[5], slot), word(wb[6], slot), word(wb[7], slot));
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars.sf_full[slot]);
+        }
+        if (r < q1 / 4) load(r + 1);
       }
     }
     ok = named_bar_and(2, 256, ok && mbar_wait(&bars.acc_full, 0, abort_flag, p.err));
@@ -337,7 +382,7 @@ struct PairParams {
   int* err;
   int T, N, KB;
   int m_tiles, n_tiles;
-  int vec32, sf_vec;  // rows aligned to 32 bytes / scale rows to 4
+  int vec32, sf_align;  // rows aligned to 32 bytes / alignment of the scale rows (16, 4, 1)
 };
 
 struct PairBars {
@@ -395,97 +440,118 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   pdl_trigger();
   pdl_wait();
 
+  // the loops over K of warps 0 and 1 are run by the whole warp, with one lane issuing
+  const uint32_t issue = lane == 0;
   if (warp == 0) {
-    if (lane == 0) {
-      int i = 0;
-      bool ok = true;
-      for (int tile = pair; tile < n_tiles && ok; tile += pairs) {
-        int mt, nt;
-        pair_tile(p, tile, mt, nt);
-        const int tok = mt * 256 + rank * 128, row = kGated ? nt * 128 : nt * 256 + rank * 128;
-        const CUtensorMap* w = &p.w[kGated ? rank : 0];
-        for (int kb = 0; kb < p.KB; ++kb, ++i) {
-          const int s = i % kPairStages;
-          if (i >= kPairStages && !(ok = mbar_wait(&bars.empty[s], (i / kPairStages - 1) & 1, abort_flag, p.err))) break;
-          uint8_t* st = ring + s * kPairStage;
-          // both CTAs' copies complete on the first CTA's barrier
-          if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * kPairStage);
-          const uint32_t full = map_cluster_rank(smem_u32(&bars.full[s]), 0);
-          tma_load_2d_pair(st, &p.x, kb * 128, tok, full);
-          tma_load_2d_pair(st + 16384, w, kb * 128, row, full);
-        }
+    RingPos at;
+    int i = 0;
+    bool ok = true;
+    const uint32_t ring0 = smem_u32(ring), full0 = map_cluster_rank(smem_u32(&bars.full[0]), 0);
+    const uint32_t expect = issue && rank == 0;
+    for (int tile = pair; tile < n_tiles && ok; tile += pairs) {
+      int mt, nt;
+      pair_tile(p, tile, mt, nt);
+      const int tok = mt * 256 + rank * 128, row = kGated ? nt * 128 : nt * 256 + rank * 128;
+      const CUtensorMap* w = &p.w[kGated ? rank : 0];
+      for (int kb = 0; kb < p.KB; ++kb, ++i) {
+        if (i >= kPairStages)
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[at.slot], at.parity ^ 1, abort_flag, p.err));
+        if (!ok) break;
+        const uint32_t st = ring0 + at.slot * kPairStage, full = full0 + 8 * at.slot;
+        // both CTAs' copies complete on the first CTA's barrier
+        mbar_expect_if(expect, &bars.full[at.slot], 2 * kPairStage);
+        tma_load_2d_pair(issue, st, &p.x, kb * 128, tok, full);
+        tma_load_2d_pair(issue, st + 16384, w, kb * 128, row, full);
+        at.next(kPairStages);
       }
-      if (rank == 0) {
-        for (int j = max(0, i - kPairStages); j < i; ++j) mbar_drain(&bars.full[j % kPairStages], (j / kPairStages) & 1);
-      } else if (!ok) {
-        // given up: the copies complete on the other CTA's barrier; leave them time to land
-        for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
-        }
+    }
+    if (rank == 0) {
+      for (int j = max(0, i - kPairStages); j < i; ++j) mbar_drain(&bars.full[j % kPairStages], (j / kPairStages) & 1);
+    } else if (!ok) {
+      // given up: the copies complete on the other CTA's barrier; leave them time to land
+      for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      int i = 0, sq = 0, it = 0;
+    if (rank == 0) {
+      RingPos at, sf;
+      uint32_t acc_parity = 1;
       bool ok = true;
-      for (int tile = pair; tile < n_tiles && ok; tile += pairs, ++it) {
-        if (it > 0 && !mbar_wait_cluster(&bars.acc_empty, (it - 1) & 1, abort_flag, p.err)) break;
-        tc_fence_after();
-        for (int kb = 0; kb < p.KB; ++kb, ++i) {
-          const int s = i % kPairStages, slot = sq % kSfSlots;
-          if ((kb & 3) == 0) ok = mbar_wait_cluster(&bars.sf_full[slot], (sq / kSfSlots) & 1, abort_flag, p.err);
-          ok = ok && mbar_wait(&bars.full[s], (i / kPairStages) & 1, abort_flag, p.err);
+      const uint32_t low0 = umma_desc_low(smem_u32(ring));
+      for (int tile = pair; tile < n_tiles && ok; tile += pairs, acc_parity ^= 1) {
+        if (tile != pair) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bars.acc_empty, acc_parity, abort_flag, p.err));
+        for (int kb = 0; kb < p.KB && ok; ++kb) {
+          if ((kb & 3) == 0) ok = mbar_wait_cluster(&bars.sf_full[sf.slot], sf.parity, abort_flag, p.err);
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(ring + s * kPairStage);
-          const uint32_t sf = tmem + kPairSfCol + slot * 12;
+          const uint32_t low = low0 + at.slot * (kPairStage >> 4);
+          const uint32_t sfa = tmem + kPairSfCol + sf.slot * 12;
           const uint32_t idesc = umma_idesc_mx8(256, 256, kb & 3);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_mx8_pair(tmem, umma_desc_sw128(st + 32 * k), umma_desc_sw128(st + 16384 + 32 * k), idesc, sf, sf + 4,
-                          (kb | k) != 0);
-          umma_commit_pair(&bars.empty[s]);
-          if ((kb & 3) == 3 || kb == p.KB - 1) umma_commit_pair(&bars.sf_empty[slot]), ++sq;
+            umma_mx8_pair(issue, tmem, umma_desc_of(low + 2 * k), umma_desc_of(low + 1024 + 2 * k), idesc, sfa, sfa + 4,
+                          k ? 1 : kb != 0);
+          umma_commit_pair(issue, &bars.empty[at.slot]);
+          at.next(kPairStages);
+          if ((kb & 3) == 3 || kb == p.KB - 1) {
+            umma_commit_pair(issue, &bars.sf_empty[sf.slot]);
+            sf.next(kSfSlots);
+          }
         }
-        if (ok) umma_commit_pair(&bars.acc_full);
+        if (ok) umma_commit_pair(issue, &bars.acc_full);
       }
-      umma_commit_pair(&bars.done);
+      umma_commit_pair(issue, &bars.done);
     }
     // the last arrival of a commit on either CTA's barriers
-    if (lane == 0) mbar_drain(&bars.done, 0);
+    mbar_drain(&bars.done, 0);
   } else if (warp < 6) {
     // scale words of this CTA's tokens (4 columns) and of all 256 weight rows (8 columns)
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
     const int blocks = (p.N + 127) / 128;
-    int sq = 0;
-    bool ok = true;
-    for (int tile = pair; tile < n_tiles && ok; tile += pairs) {
+    uint4 a[4], u, v;
+    auto load = [&](int tile, int r) {
       int mt, nt;
       pair_tile(p, tile, mt, nt);
       const int tok0 = mt * 256 + rank * 128 + lane;
       const int b0 = kGated ? nt : 2 * nt, b1 = kGated ? nt : 2 * nt + 1;
-      const uint8_t* w0 = p.sw[0] + int64_t(b0) * p.KB;
-      const uint8_t* w1 = p.sw[kGated ? 1 : 0] + int64_t(b1) * p.KB;
-      for (int q = 0; q < nq; ++q, ++sq) {
-        const int slot = sq % kSfSlots;
-        uint32_t a[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          a[c] = tok0 + 32 * c < p.T ? scale_word(p.sx + int64_t(tok0 + 32 * c) * p.KB, q, p.KB, p.sf_vec) : 0x7f7f7f7fu;
-        const uint32_t u = scale_word(w0, q, p.KB, p.sf_vec);
-        const uint32_t v = b1 < blocks ? scale_word(w1, q, p.KB, p.sf_vec) : 0x7f7f7f7fu;
-        if (sq >= kSfSlots) {
-          ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (sq / kSfSlots - 1) & 1, abort_flag, p.err));
-          if (!ok) break;
-          tc_fence_after();
+      for (int c = 0; c < 4; ++c) {
+        a[c] = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
+        if (tok0 + 32 * c < p.T) a[c] = scale_round(p.sx + int64_t(tok0 + 32 * c) * p.KB, r, p.KB, p.sf_align);
+      }
+      u = scale_round(p.sw[0] + int64_t(b0) * p.KB, r, p.KB, p.sf_align);
+      v = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
+      if (b1 < blocks) v = scale_round(p.sw[kGated ? 1 : 0] + int64_t(b1) * p.KB, r, p.KB, p.sf_align);
+    };
+    int sq = 0;
+    bool ok = true;
+    if (pair < n_tiles) load(pair, 0);
+    for (int tile = pair; tile < n_tiles && ok; tile += pairs) {
+      for (int q = 0; q < nq && ok; q += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (q + i >= nq) break;
+          const int slot = sq % kSfSlots;
+          if (sq >= kSfSlots) {
+            ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (sq / kSfSlots - 1) & 1, abort_flag, p.err));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          const uint32_t sf = tmem + quarter + kPairSfCol + slot * 12;
+          const uint32_t uw = word(u, i), vw = word(v, i);
+          tmem_st4(sf, word(a[0], i), word(a[1], i), word(a[2], i), word(a[3], i));
+          tmem_st4(sf + 4, uw, uw, uw, uw);
+          tmem_st4(sf + 8, vw, vw, vw, vw);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(map_cluster_rank(smem_u32(&bars.sf_full[slot]), 0));
+          ++sq;
         }
-        const uint32_t sf = tmem + quarter + kPairSfCol + slot * 12;
-        tmem_st4(sf, a[0], a[1], a[2], a[3]);
-        tmem_st4(sf + 4, u, u, u, u);
-        tmem_st4(sf + 8, v, v, v, v);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_cluster_rank(smem_u32(&bars.sf_full[slot]), 0));
+        // the next round, or the first of the next tile
+        if (q + 4 < nq) load(tile, q / 4 + 1);
+        else if (tile + pairs < n_tiles) load(tile + pairs, 0);
       }
     }
   } else {
@@ -673,7 +739,7 @@ int launch_pair(const scion_fp8* L, const StreamParams& q, const uint8_t* x, int
   PairParams p{};
   p.w[0] = L->w[0], p.w[1] = L->w[kGated ? 1 : 0];
   p.sw[0] = q.sw[0], p.sw[1] = q.sw[1], p.sx = q.sx, p.base = q.base, p.out = q.out, p.codes = q.codes;
-  p.scales = q.scales, p.err = q.err, p.T = T, p.N = q.N, p.KB = q.KB, p.sf_vec = q.sf_vec;
+  p.scales = q.scales, p.err = q.err, p.T = T, p.N = q.N, p.KB = q.KB, p.sf_align = q.sf_align;
   p.m_tiles = (T + 255) / 256, p.n_tiles = kGated ? (p.N + 127) / 128 : (p.N + 255) / 256;
   p.vec32 = int64_t(p.N) * kElem % 32 == 0 && !misaligned(p.out, 32);
   int st = make_tmap_codes(&p.x, x, T, L->desc.k, 128);
@@ -687,7 +753,9 @@ StreamParams params(const scion_fp8* L, const uint8_t* sx, int T) {
   StreamParams p{};
   p.sx = sx, p.sw[0] = L->desc.w_scales, p.sw[1] = L->desc.up_scales;
   p.T = T, p.N = L->desc.n, p.KB = (L->desc.k + 127) / 128, p.err = L->err;
-  p.sf_vec = p.KB % 4 == 0 && !misaligned(sx, 4) && !misaligned(p.sw[0], 4) && !misaligned(p.sw[1], 4);
+  p.sf_align = 1;
+  for (int a : {4, 16})
+    if (p.KB % a == 0 && !misaligned(sx, a) && !misaligned(p.sw[0], a) && !misaligned(p.sw[1], a)) p.sf_align = a;
   return p;
 }
 
