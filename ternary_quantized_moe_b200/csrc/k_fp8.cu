@@ -191,24 +191,24 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
   pdl_wait();
 
   bool joined = splits == 1;
-  // the loops over K of warps 0 and 1 are run by the whole warp, with one lane issuing
-  const uint32_t issue = lane == 0;
+  // the loops over K of warps 0 and 1 are run by the whole warp, with one lane (elect_one) issuing
   if (warp == 0) {
     RingPos at;
     int i = 0;
-    const uint32_t ring0 = smem_u32(ring);
-    uint32_t st = ring0;
+    uint8_t* st = ring;
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb, ++i) {
       if (i >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[at.slot], at.parity ^ 1, abort_flag, p.err));
       if (!ok) break;
       uint64_t* full = &bars.full[at.slot];
-      mbar_expect_if(issue, full, stage_bytes);
-      tma_load_2d_if(issue, st, &p.w[0], kb * 128, row0, full);
-      if (NW == 2) tma_load_2d_if(issue, st + 16384, &p.w[1], kb * 128, row0, full);
-      tma_load_2d_if(issue, st + NW * 16384, &p.x, kb * 128, tok0, full);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full, stage_bytes);
+        tma_load_2d(st, &p.w[0], kb * 128, row0, full);
+        if (NW == 2) tma_load_2d(st + 16384, &p.w[1], kb * 128, row0, full);
+        tma_load_2d(st + NW * 16384, &p.x, kb * 128, tok0, full);
+      }
       at.next(p.stages);
-      st = at.slot ? st + stage_bytes : ring0;
+      st = at.slot ? st + stage_bytes : ring;
     }
     // copies may still be in flight if the MMA warp gave up
     for (int j = max(0, i - p.stages); j < i; ++j) mbar_drain(&bars.full[j % p.stages], (j / p.stages) & 1);
@@ -226,22 +226,26 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
       tc_fence_after();
       const uint32_t sf = tmem + p.sf_col + slot * (4 * NW + p.sfb_cols);
       const uint32_t idesc = umma_idesc_mx8(128, p.bn, kb & 3);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int m = 0; m < NW; ++m)
-          umma_mx8(issue, tmem + m * p.bn, umma_desc_of(low + m * 1024 + 2 * k), umma_desc_of(low + NW * 1024 + 2 * k),
-                   idesc, sf + 4 * m, sf + 4 * NW, k ? 1 : accumulate);
+          for (int m = 0; m < NW; ++m)
+            umma_mx8(tmem + m * p.bn, umma_desc_of(low + m * 1024 + 2 * k), umma_desc_of(low + NW * 1024 + 2 * k), idesc,
+                     sf + 4 * m, sf + 4 * NW, k ? 1 : accumulate);
+        }
+        umma_commit(&bars.empty[at.slot]);
+        if ((kb & 3) == 3) umma_commit(&bars.sf_empty[slot]);
       }
       accumulate = 1;
-      umma_commit_if(issue, &bars.empty[at.slot]);
-      if ((kb & 3) == 3) umma_commit_if(issue, &bars.sf_empty[slot]);
       at.next(p.stages);
       low = at.slot ? low + (stage_bytes >> 4) : low0;
     }
-    if (ok) umma_commit_if(issue, &bars.acc_full);
+    if (elect_one()) {
+      if (ok) umma_commit(&bars.acc_full);
+      umma_commit(&bars.done);
+    }
     // every MMA issued above has finished before tensor memory is released
-    umma_commit_if(issue, &bars.done);
     mbar_drain(&bars.done, 0);
   } else {
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
@@ -440,14 +444,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   pdl_trigger();
   pdl_wait();
 
-  // the loops over K of warps 0 and 1 are run by the whole warp, with one lane issuing
-  const uint32_t issue = lane == 0;
+  // the loops over K of warps 0 and 1 are run by the whole warp, with one lane (elect_one) issuing
   if (warp == 0) {
     RingPos at;
     int i = 0;
     bool ok = true;
     const uint32_t ring0 = smem_u32(ring), full0 = map_cluster_rank(smem_u32(&bars.full[0]), 0);
-    const uint32_t expect = issue && rank == 0;
     for (int tile = pair; tile < n_tiles && ok; tile += pairs) {
       int mt, nt;
       pair_tile(p, tile, mt, nt);
@@ -459,9 +461,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         if (!ok) break;
         const uint32_t st = ring0 + at.slot * kPairStage, full = full0 + 8 * at.slot;
         // both CTAs' copies complete on the first CTA's barrier
-        mbar_expect_if(expect, &bars.full[at.slot], 2 * kPairStage);
-        tma_load_2d_pair(issue, st, &p.x, kb * 128, tok, full);
-        tma_load_2d_pair(issue, st + 16384, w, kb * 128, row, full);
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&bars.full[at.slot], 2 * kPairStage);
+          tma_load_2d_pair(st, &p.x, kb * 128, tok, full);
+          tma_load_2d_pair(st + 16384, w, kb * 128, row, full);
+        }
         at.next(kPairStages);
       }
     }
@@ -488,20 +492,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
           const uint32_t low = low0 + at.slot * (kPairStage >> 4);
           const uint32_t sfa = tmem + kPairSfCol + sf.slot * 12;
           const uint32_t idesc = umma_idesc_mx8(256, 256, kb & 3);
+          const bool last = (kb & 3) == 3 || kb == p.KB - 1;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_mx8_pair(issue, tmem, umma_desc_of(low + 2 * k), umma_desc_of(low + 1024 + 2 * k), idesc, sfa, sfa + 4,
-                          k ? 1 : kb != 0);
-          umma_commit_pair(issue, &bars.empty[at.slot]);
-          at.next(kPairStages);
-          if ((kb & 3) == 3 || kb == p.KB - 1) {
-            umma_commit_pair(issue, &bars.sf_empty[sf.slot]);
-            sf.next(kSfSlots);
+            for (int k = 0; k < 4; ++k)
+              umma_mx8_pair(tmem, umma_desc_of(low + 2 * k), umma_desc_of(low + 1024 + 2 * k), idesc, sfa, sfa + 4,
+                            k ? 1 : kb != 0);
+            umma_commit_pair(&bars.empty[at.slot]);
+            if (last) umma_commit_pair(&bars.sf_empty[sf.slot]);
           }
+          at.next(kPairStages);
+          if (last) sf.next(kSfSlots);
         }
-        if (ok) umma_commit_pair(issue, &bars.acc_full);
+        if (ok && elect_one()) umma_commit_pair(&bars.acc_full);
       }
-      umma_commit_pair(issue, &bars.done);
+      if (elect_one()) umma_commit_pair(&bars.done);
     }
     // the last arrival of a commit on either CTA's barriers
     mbar_drain(&bars.done, 0);
