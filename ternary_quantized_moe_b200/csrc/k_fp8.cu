@@ -219,11 +219,12 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
     uint32_t low = low0, accumulate = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
       const int slot = (kb >> 2) % kSfSlots;
-      if (kb == kb0 || (kb & 3) == 0)  // (a slot's phase turns over every four words)
+      if (kb == kb0 || (kb & 3) == 0) {  // (a slot's phase turns over every four words)
         ok = mbar_wait(&bars.sf_full[slot], ((kb >> 2) - (kb0 >> 2)) / kSfSlots & 1, abort_flag, p.err);
+        tc_fence_after();
+      }
       ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
       if (!ok) break;
-      tc_fence_after();
       const uint32_t sf = tmem + p.sf_col + slot * (4 * NW + p.sfb_cols);
       const uint32_t idesc = umma_idesc_mx8(128, p.bn, kb & 3);
       if (elect_one()) {
@@ -485,10 +486,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       for (int tile = pair; tile < n_tiles && ok; tile += pairs, acc_parity ^= 1) {
         if (tile != pair) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bars.acc_empty, acc_parity, abort_flag, p.err));
         for (int kb = 0; kb < p.KB && ok; ++kb) {
-          if ((kb & 3) == 0) ok = mbar_wait_cluster(&bars.sf_full[sf.slot], sf.parity, abort_flag, p.err);
+          if ((kb & 3) == 0) {
+            ok = mbar_wait_cluster(&bars.sf_full[sf.slot], sf.parity, abort_flag, p.err);
+            tc_fence_after();
+          }
           ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
           if (!ok) break;
-          tc_fence_after();
           const uint32_t low = low0 + at.slot * (kPairStage >> 4);
           const uint32_t sfa = tmem + kPairSfCol + sf.slot * 12;
           const uint32_t idesc = umma_idesc_mx8(256, 256, kb & 3);
