@@ -366,11 +366,12 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
 // each CTA loads half of the weight rows, which halves the shared-memory traffic of B.  A gated tile
 // is 128 gate rows (first CTA) and the 128 up rows of the same features (second CTA).  Persistent:
 // the pairs walk the tiles in groups of 8 token tiles, so that the operands in use stay in L2.
-// Roles: warp 0 TMA loads, warp 1 the MMAs (first CTA only), warps 2..5 the scale words, warps 6..13
-// the epilogue (two per lane quarter, each half of the 256 columns).  The 256 accumulator columns
-// are drained into registers and released before anything is stored, so the next tile's MMAs wait
-// for the drain alone.
-constexpr int kPairThreads = 14 * 32;
+// Roles by warpgroup: warp 0 TMA loads and warp 1 the MMAs (first CTA only); warps 4..7 the scale
+// words; warps 8..15 the epilogue (two per lane quarter, each half of the 256 columns).  The 256
+// accumulator columns are drained into registers (128 per thread) and released before anything is
+// computed or stored, so the next tile's MMAs wait for the drain alone; the registers come from the
+// other two warpgroups (128 x (48 + 48 + 208 + 208) = the 512 x 128 launched).
+constexpr int kPairThreads = 512;
 constexpr int kPairStages = 6;
 constexpr int kPairStage = 2 * 16384;  // per CTA: 128 token rows, 128 weight rows, 128 columns
 constexpr int kPairSfCol = 256;        // scale words behind the accumulators: 4 + 8 columns per slot
@@ -387,7 +388,7 @@ struct PairParams {
   int* err;
   int T, N, KB;
   int m_tiles, n_tiles;
-  int vec32, sf_align;  // rows aligned to 32 bytes / alignment of the scale rows (16, 4, 1)
+  int out_bf16, sf_align;  // sf_align: alignment of the scale rows (16, 4, 1)
 };
 
 struct PairBars {
@@ -397,7 +398,7 @@ struct PairBars {
   uint32_t amax[2][2][128];  // [tile parity][column half][token]
 };
 
-enum PairEpi { kPairBf16 = 0, kPairF32 = 1, kPairGatedBf16 = 2, kPairGatedCodes = 3 };
+enum PairEpi { kPairBf16 = 0, kPairF32 = 1, kPairBase = 2, kPairGatedBf16 = 3, kPairGatedCodes = 4 };
 
 __device__ __forceinline__ void pair_tile(const PairParams& p, int i, int& mt, int& nt) {
   const int per = kPairGroup * p.n_tiles, g = i / per, r = i - g * per;
@@ -405,24 +406,74 @@ __device__ __forceinline__ void pair_tile(const PairParams& p, int i, int& mt, i
   nt = r / rows, mt = g * kPairGroup + r - nt * rows;
 }
 
-__device__ __forceinline__ void store32(void* dst, const uint32_t* v, bool whole) {
-  if (whole) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+// One warp's 32 token rows x 128 columns, one row per thread in `v`, to global memory.  A chunk of
+// 128 bytes per row goes through 4 KB of shared memory (16-byte pieces, XOR-swizzled by row, so both
+// sides are conflict-free), and leaves as whole lines: 8 lanes per row, 4 rows per instruction.
+// kElem: bytes per staged element (4: fp32, 2: bf16 pairs packed before staging); with a base the
+// sums are staged as fp32 and the base is read in the same pattern, one chunk ahead.
+struct RowsOut {
+  const float* base;
+  uint8_t* out;
+  int64_t tok;  // first token
+  int n0, T, N, out_bf16;
+};
+
+template <bool kBase>
+__device__ __forceinline__ void load_base(const RowsOut& o, int chunk, int lane, float4 (&b)[8]) {
+  if (!kBase) return;
+  const int n = o.n0 + chunk * 32 + (lane & 7) * 4;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t t = o.tok + 4 * i + (lane >> 3);
+    b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < o.T && n < o.N) b[i] = *reinterpret_cast<const float4*>(o.base + t * o.N + n);
+  }
+}
+
+template <int kElem, bool kBase>
+__device__ __forceinline__ void store_rows(const RowsOut& o, const uint32_t (&v)[128], uint32_t stage, int lane,
+                                           float4 (&b)[8]) {
+  constexpr int kCols = 128 / kElem;
+#pragma unroll
+  for (int c = 0; c < 128 / kCols; ++c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = c * kCols + (4 * i + j) * (4 / kElem);
+        w[j] = kElem == 4 ? v[e & 127] : pack_bf16x2(__uint_as_float(v[e & 127]), __uint_as_float(v[(e + 1) & 127]));
+      }
+      sts_v4(stage + lane * 128 + ((i ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    const int n = o.n0 + c * kCols + (lane & 7) * (16 / kElem);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const int64_t t = o.tok + r;
+      float4 x = lds_f4(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+      if (kBase) x.x += b[i].x, x.y += b[i].y, x.z += b[i].z, x.w += b[i].w;
+      if (t < o.T && n < o.N) {
+        if (kBase && o.out_bf16)
+          *reinterpret_cast<uint2*>(o.out + (t * o.N + n) * 2) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+        else
+          *reinterpret_cast<float4*>(o.out + (t * o.N + n) * kElem) = x;
+      }
+    }
+    __syncwarp();
+    if (c + 1 < 128 / kCols) load_base<kBase>(o, c + 1, lane, b);
   }
 }
 
 template <int EPI>
 __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_constant__ PairParams p) {
   constexpr bool kGated = EPI == kPairGatedBf16 || EPI == kPairGatedCodes;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  static_assert(kPairStages * kPairStage + 32768 + sizeof(PairBars) <= kSmem, "shared memory");
   uint8_t* ring = smem;
-  PairBars& bars = *reinterpret_cast<PairBars*>(smem + kPairStages * kPairStage);
+  const uint32_t staging = smem_u32(ring) + kPairStages * kPairStage;
+  PairBars& bars = *reinterpret_cast<PairBars*>(smem + kPairStages * kPairStage + 32768);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int n_tiles = p.m_tiles * p.n_tiles, nq = (p.KB + 3) / 4;
@@ -446,6 +497,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   pdl_wait();
 
   // the loops over K of warps 0 and 1 are run by the whole warp, with one lane (elect_one) issuing
+  if (warp < 4) regs_down<48>();
   if (warp == 0) {
     RingPos at;
     int i = 0;
@@ -513,7 +565,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     }
     // the last arrival of a commit on either CTA's barriers
     mbar_drain(&bars.done, 0);
-  } else if (warp < 6) {
+  } else if (warp < 4) {
+  } else if (warp < 8) {
+    regs_down<48>();
     // scale words of this CTA's tokens (4 columns) and of all 256 weight rows (8 columns)
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
     const int blocks = (p.N + 127) / 128;
@@ -563,86 +617,50 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       }
     }
   } else {
-    const int quarter = warp & 3, half = (warp - 6) >> 2;
+    regs_up<208>();
+    const int quarter = warp & 3, half = (warp - 8) >> 2;
     const int row = quarter * 32 + lane;
-    const uint32_t acc = tmem + (uint32_t(quarter * 32) << 16);
+    // plain: 128 consecutive columns; gated: 64 gate columns and the up columns of the same features
+    const uint32_t acc0 = tmem + (uint32_t(quarter * 32) << 16) + half * (kGated ? 64 : 128);
+    const uint32_t acc1 = acc0 + (kGated ? 128 : 64);
     const uint32_t released = map_cluster_rank(smem_u32(&bars.acc_empty), 0);
-    int it = 0;
-    for (int tile = pair; tile < n_tiles; tile += pairs, ++it) {
+    uint32_t parity = 0;
+    for (int tile = pair; tile < n_tiles; tile += pairs, parity ^= 1) {
       int mt, nt;
       pair_tile(p, tile, mt, nt);
-      if (!named_bar_and(2, 256, mbar_wait(&bars.acc_full, it & 1, abort_flag, p.err))) break;
+      const RowsOut rows{p.base, static_cast<uint8_t*>(p.out), int64_t(mt) * 256 + rank * 128 + quarter * 32,
+                         nt * 256 + half * 128, p.T, p.N, p.out_bf16};
+      float4 base[8];
+      load_base<EPI == kPairBase>(rows, 0, lane, base);  // (in flight during the tile's MMAs)
+      if (!named_bar_and(2, 256, mbar_wait(&bars.acc_full, parity, abort_flag, p.err))) break;
       tc_fence_after();
+      uint32_t v[128];
+      tmem_ld64x2(acc0, acc1, v);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(released);
       const int64_t tok = int64_t(mt) * 256 + rank * 128 + row;
       const bool live = tok < p.T;
-      if (EPI == kPairBf16 || EPI == kPairF32) {
-        const int n0 = nt * 256 + half * 128;
-        // bf16: all 128 columns wait packed in registers; fp32: the first half is stored before the
-        // second is loaded
-        uint32_t v[64];
-        for (int part = 0; part < (EPI == kPairF32 ? 2 : 1); ++part) {
-#pragma unroll
-          for (int c = 0; c < (EPI == kPairF32 ? 2 : 4); ++c) {
-            const int col = part * 64 + 32 * c;
-            float f[32];
-            tmem_ld32(acc + half * 128 + col, f);
-            if (p.base && live) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (n0 + col + 4 * j < p.N) {
-                  const float4 b = *reinterpret_cast<const float4*>(p.base + tok * p.N + n0 + col + 4 * j);
-                  f[4 * j] += b.x, f[4 * j + 1] += b.y, f[4 * j + 2] += b.z, f[4 * j + 3] += b.w;
-                }
-            }
-            if (EPI == kPairF32) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[32 * (c & 1) + j] = __float_as_uint(f[j]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[16 * c + j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-            }
-          }
-          if (EPI == kPairBf16 || part == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(released);
-          }
-          if (live) {
-            constexpr int kElem = EPI == kPairF32 ? 4 : 2;
-            uint8_t* dst = static_cast<uint8_t*>(p.out) + (tok * p.N + n0 + part * 64) * kElem;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int n = n0 + part * 64 + j * (32 / kElem);
-              if (n + 32 / kElem <= p.N) store32(dst + 32 * j, v + 8 * j, p.vec32);
-              else if (n < p.N)  // N is a multiple of 16 bytes
-                *reinterpret_cast<uint4*>(dst + 32 * j) = make_uint4(v[8 * j], v[8 * j + 1], v[8 * j + 2], v[8 * j + 3]);
-            }
-          }
-        }
+      if (!kGated) {
+        store_rows<EPI == kPairBf16 ? 2 : 4, EPI == kPairBase>(rows, v, staging + (warp - 8) * 4096, lane, base);
       } else {
-        // gate columns half * 64 .. + 63 and the up columns 128 behind them
         const int f0 = nt * 128 + half * 64;
         float h[64];
         uint32_t m = 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float g[16], u[16];
-          tmem_ld16x2(acc + half * 64 + 16 * c, acc + 128 + half * 64 + 16 * c, g, u);
           const bool in = f0 + 16 * c < p.N;  // N is a multiple of 16
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            h[16 * c + j] = silu_mul(g[j], u[j]);
-            m = max(m, in ? mag(h[16 * c + j]) : 0u);
+          for (int j = 16 * c; j < 16 * c + 16; ++j) {
+            h[j] = silu_mul(__uint_as_float(v[j]), __uint_as_float(v[64 + j]));
+            m = max(m, in ? mag(h[j]) : 0u);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(released);
         if (EPI == kPairGatedCodes) {
           // the group's other 64 features are with the thread of the other half
-          bars.amax[it & 1][half][row] = m;
+          bars.amax[parity][half][row] = m;
           asm volatile("bar.sync 3, 256;" ::: "memory");
-          const uint32_t b = scale_byte(max(m, bars.amax[it & 1][half ^ 1][row]));
+          const uint32_t b = scale_byte(max(m, bars.amax[parity][half ^ 1][row]));
           const float inv = scale_inverse(b);
           if (live) {
             uint8_t* dst = p.codes + tok * p.N + f0;
@@ -663,10 +681,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             if (f0 + 16 * c >= p.N) continue;
-            uint32_t v[8];
+            uint32_t o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = pack_bf16x2(h[16 * c + 2 * j], h[16 * c + 2 * j + 1]);
-            store32(dst + 32 * c, v, p.vec32);
+            for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(h[16 * c + 2 * j], h[16 * c + 2 * j + 1]);
+            reinterpret_cast<uint4*>(dst + 32 * c)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            reinterpret_cast<uint4*>(dst + 32 * c)[1] = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
       }
@@ -743,13 +762,12 @@ bool use_pair(const scion_fp8* L, int T, bool aligned) {
 template <int EPI>
 int launch_pair(const scion_fp8* L, const StreamParams& q, const uint8_t* x, int T, cudaStream_t s) {
   constexpr bool kGated = EPI == kPairGatedBf16 || EPI == kPairGatedCodes;
-  constexpr int kElem = EPI == kPairF32 ? 4 : 2;
   PairParams p{};
   p.w[0] = L->w[0], p.w[1] = L->w[kGated ? 1 : 0];
   p.sw[0] = q.sw[0], p.sw[1] = q.sw[1], p.sx = q.sx, p.base = q.base, p.out = q.out, p.codes = q.codes;
   p.scales = q.scales, p.err = q.err, p.T = T, p.N = q.N, p.KB = q.KB, p.sf_align = q.sf_align;
   p.m_tiles = (T + 255) / 256, p.n_tiles = kGated ? (p.N + 127) / 128 : (p.N + 255) / 256;
-  p.vec32 = int64_t(p.N) * kElem % 32 == 0 && !misaligned(p.out, 32);
+  p.out_bf16 = q.out_bf16;
   int st = make_tmap_codes(&p.x, x, T, L->desc.k, 128);
   if (st != SCION_OK) return st;
   const int64_t tiles = int64_t(p.m_tiles) * p.n_tiles;
@@ -795,7 +813,7 @@ extern "C" int scion_fp8_create(const scion_fp8_desc* D, void* stream, scion_fp8
   for (const auto f : {scion::fp8_stream_kernel<1>, scion::fp8_stream_kernel<2>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, scion::kSmem);
   for (const auto f : {scion::fp8_pair_kernel<scion::kPairBf16>, scion::fp8_pair_kernel<scion::kPairF32>,
-                       scion::fp8_pair_kernel<scion::kPairGatedBf16>, scion::fp8_pair_kernel<scion::kPairGatedCodes>})
+                       scion::fp8_pair_kernel<scion::kPairBase>, scion::fp8_pair_kernel<scion::kPairGatedBf16>, scion::fp8_pair_kernel<scion::kPairGatedCodes>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, scion::kSmem);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&L->err), sizeof(int));
   if (e == cudaSuccess) e = cudaMemsetAsync(L->err, 0, sizeof(int), static_cast<cudaStream_t>(stream));
@@ -830,8 +848,9 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool rows16 = int64_t(p.N) * (p.out_bf16 ? 2 : 4) % 16 == 0 && p.vec;
   if (scion::use_pair(L, T, rows16))
-    return p.out_bf16 ? scion::launch_pair<scion::kPairBf16>(L, p, x_codes, T, s)
-                      : scion::launch_pair<scion::kPairF32>(L, p, x_codes, T, s);
+    return base         ? scion::launch_pair<scion::kPairBase>(L, p, x_codes, T, s)
+           : p.out_bf16 ? scion::launch_pair<scion::kPairBf16>(L, p, x_codes, T, s)
+                        : scion::launch_pair<scion::kPairF32>(L, p, x_codes, T, s);
   return scion::launch_stream<1>(L, p, x_codes, T, s);
 }
 
