@@ -30,12 +30,14 @@ typedef __nv_bfloat16 bf16;
 // Few tokens: bound by reading the weights once.  The weights are the M side (128 rows per tile),
 // the tokens the N side (bn of them, a multiple of 16), and the CTAs of a cluster split K, so that a
 // matrix of few tiles still spreads over the SMs.  Partial sums: the tokens of a tile are dealt to
-// the CTAs of the cluster in groups of four; every CTA stores its sums of a group straight into the
-// shared memory of the group's owner (every warp then arrives on a barrier there), and the owner
-// adds them in rank order.  One barrier of the cluster, at the start, and none on the way out: an
-// owner leaves when everything sent to it has arrived.
+// the CTAs of the cluster; every CTA stores its sums of a token straight into the shared memory of
+// the token's owner (every warp then arrives on a barrier there), and the owner adds them in rank
+// order.  One barrier of the cluster, at the start, and none on the way out: an owner leaves when
+// everything sent to it has arrived.
 // Roles: warp 0 TMA loads through a ring of 128-column stages, warp 1 the MMAs, warps 2..9 the
-// epilogue (two per lane quarter, alternate 16-token chunks), warps 2..5 also the scale words.
+// epilogue (two per lane quarter, alternate 16-token chunks), warps 2..5 also the scale words.  The
+// sums pass through shared memory, so that a warp finishes one token at a time with four features
+// per lane: one reduction for a token's scale, 128 features in whole sectors.
 constexpr int kStreamThreads = 320;
 constexpr int kMaxStages = 12;
 constexpr int kSfSlots = 4;  // ring of scale words, each slot for 4 K blocks (one byte each)
@@ -60,7 +62,6 @@ struct Bars {
   uint64_t full[kMaxStages], empty[kMaxStages], sf_full[kSfSlots], sf_empty[kSfSlots], acc_full, done, sums;
   uint32_t tmem_slot;
   int abort_flag;
-  uint32_t amax[2][2][16][4];  // [thread group][parity][token][lane quarter]
 };
 
 // Scale bytes of one row are read 16 K blocks at a time (a "round": four words of four blocks), so
@@ -95,79 +96,101 @@ struct RingPos {
   }
 };
 
-// Four floats into the shared memory of another CTA of the cluster (or this one).
-__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float a, float b, float c, float d) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+// A float into the shared memory of another CTA of the cluster (or this one).
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
-// The results of one feature (of the 128 a group of four warps holds) for NT tokens from t on.
-// `live`: tokens t .. t + live - 1 exist.  All 128 threads of the group take part.
-template <int NW, int NT>
-__device__ __forceinline__ void stream_store(const StreamParams& p, Bars& bars, const float (&a)[NT], const float (&b)[NT],
-                                             int64_t t, int live, int group, int& parity) {
-  const int quarter = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  const int n = blockIdx.y * 128 + quarter * 32 + lane;
-  const bool in = n < p.N;
-  const int64_t at = t * p.N + n;
+// The results of `count` (at most B) tokens t, t + step, ...: features n .. n + 3 of this lane.
+template <int NW, int B>
+__device__ __forceinline__ void store_tokens(const StreamParams& p, float4 (&v)[B][NW], int t, int step, int count, int n,
+                                             int lane) {
   if (NW == 1) {
-    if (!in) return;
+    if (p.vec) {  // N a multiple of 4, rows aligned: all four or none
+      if (n >= p.N) return;
+      if (p.base) {
+        float4 b[B];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      if (i >= live) break;
-      const int64_t o = at + int64_t(i) * p.N;
-      const float v = p.base ? p.base[o] + a[i] : a[i];
-      if (p.out_bf16) static_cast<bf16*>(p.out)[o] = __float2bfloat16_rn(v);
-      else static_cast<float*>(p.out)[o] = v;
+        for (int i = 0; i < B; ++i)
+          if (i < count) b[i] = *reinterpret_cast<const float4*>(p.base + int64_t(t + i * step) * p.N + n);
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+          if (i < count) v[i][0].x += b[i].x, v[i][0].y += b[i].y, v[i][0].z += b[i].z, v[i][0].w += b[i].w;
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        if (i >= count) break;
+        const int64_t at = int64_t(t + i * step) * p.N + n;
+        const float4 o = v[i][0];
+        if (p.out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<bf16*>(p.out) + at) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = o;
+      }
+      return;
+    }
+    for (int i = 0; i < B; ++i) {
+      if (i >= count) break;
+      const int64_t at = int64_t(t + i * step) * p.N + n;
+      const float o[4] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (n + j >= p.N) break;
+        const float s = p.base ? p.base[at + j] + o[j] : o[j];
+        if (p.out_bf16) static_cast<bf16*>(p.out)[at + j] = __float2bfloat16_rn(s);
+        else static_cast<float*>(p.out)[at + j] = s;
+      }
     }
     return;
   }
-  float h[NT];
+  uint32_t m[B];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) h[i] = silu_mul(a[i], b[i]);
+  for (int i = 0; i < B; ++i) {
+    const float4 g = v[i][0], u = v[i][NW - 1];
+    v[i][0] = make_float4(silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w));
+    m[i] = max(max(mag(v[i][0].x), mag(v[i][0].y)), max(mag(v[i][0].z), mag(v[i][0].w)));
+  }
   if (p.codes) {
-    // the largest magnitude over the 128 features: within the warps, then over the four of them
-    uint32_t(*amax)[4] = bars.amax[group][parity];
-    parity ^= 1;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, in ? mag(h[i]) : 0u);
-      if (lane == i) amax[i][quarter] = m;
+    for (int i = 0; i < B; ++i) m[i] = __reduce_max_sync(0xffffffffu, n < p.N ? m[i] : 0u);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (i >= count) break;
+      const int64_t tok = t + i * step;
+      const uint32_t b = scale_byte(m[i]);
+      const float inv = scale_inverse(b);
+      const float4 h = v[i][0];
+      if (n < p.N) *reinterpret_cast<uint32_t*>(p.codes + tok * p.N + n) = pack4(h.x * inv, h.y * inv, h.z * inv, h.w * inv);
+      if (lane == 0) p.scales[tok * ((p.N + 127) / 128) + blockIdx.y] = uint8_t(b);
     }
-    asm volatile("bar.sync %0, 128;" ::"r"(4 + group) : "memory");
+  } else if (n < p.N) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      if (i >= live) break;
-      const uint4 m = *reinterpret_cast<const uint4*>(amax[i]);
-      const uint32_t s = scale_byte(max(max(m.x, m.y), max(m.z, m.w)));
-      if (in) p.codes[at + int64_t(i) * p.N] = uint8_t(pack4(h[i] * scale_inverse(s), 0.f, 0.f, 0.f));
-      if (quarter == 0 && lane == 0) p.scales[(t + i) * ((p.N + 127) / 128) + blockIdx.y] = uint8_t(s);
-    }
-  } else if (in) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      if (i >= live) break;
-      static_cast<bf16*>(p.out)[at + int64_t(i) * p.N] = __float2bfloat16_rn(h[i]);
+    for (int i = 0; i < B; ++i) {
+      if (i >= count) break;
+      const float4 h = v[i][0];
+      *reinterpret_cast<uint2*>(static_cast<bf16*>(p.out) + int64_t(t + i * step) * p.N + n) =
+          make_uint2(pack_bf16x2(h.x, h.y), pack_bf16x2(h.z, h.w));
     }
   }
 }
 
 // NW = 1: out = base + W x.  NW = 2: h = silu(W0 x) (W1 x), to bf16 or codes and scales.
 template <int NW>
-__global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid_constant__ StreamParams p) {
+__global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __grid_constant__ StreamParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars& bars = *reinterpret_cast<Bars*>(smem);
-  uint8_t* ring = smem + 2048;
+  uint8_t* ring = smem + 1024;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x, splits = gridDim.x;
   const int row0 = blockIdx.y * 128, tok0 = blockIdx.z * p.bn;
   const int kb0 = int(int64_t(rank) * p.KB / splits), kb1 = int(int64_t(rank + 1) * p.KB / splits);
   const uint32_t stage_bytes = NW * 16384 + p.bn * 128;
-  const int nt = min(p.bn, p.T - tok0), quads = (nt + 3) / 4;
-  // this CTA's groups of four tokens and what arrives for them: [group][sender][matrix][feature][4]
-  const int mine = rank < quads ? (quads - rank + splits - 1) / splits : 0;
+  const int nt = min(p.bn, p.T - tok0);
+  // this CTA's tokens (rank, rank + splits, ...) and what arrives for them: [token][sender][matrix][feature]
+  const int mine = rank < nt ? (nt - rank + splits - 1) / splits : 0;
   const uint32_t sums = smem_u32(ring + p.stages * stage_bytes);
 
   if (threadIdx.x == 0) {
@@ -217,16 +240,23 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
     bool ok = true;
     const uint32_t low0 = umma_desc_low(smem_u32(ring));
     uint32_t low = low0, accumulate = 0;
+    // (the next stage's barrier is tested while the MMAs of this one are issued: a test and the vote on
+    // it take as long as three MMAs of 64 tokens)
+    bool ready = false;
     for (int kb = kb0; kb < kb1; ++kb) {
       const int slot = (kb >> 2) % kSfSlots;
       if (kb == kb0 || (kb & 3) == 0) {  // (a slot's phase turns over every four words)
-        ok = mbar_wait(&bars.sf_full[slot], ((kb >> 2) - (kb0 >> 2)) / kSfSlots & 1, abort_flag, p.err);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.sf_full[slot], ((kb >> 2) - (kb0 >> 2)) / kSfSlots & 1, abort_flag, p.err));
         tc_fence_after();
       }
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
+      if (!__all_sync(0xffffffffu, ready))
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
       if (!ok) break;
       const uint32_t sf = tmem + p.sf_col + slot * (4 * NW + p.sfb_cols);
       const uint32_t idesc = umma_idesc_mx8(128, p.bn, kb & 3);
+      uint64_t* empty = &bars.empty[at.slot];
+      at.next(p.stages);
+      ready = mbar_test(&bars.full[at.slot], at.parity);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -235,11 +265,10 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
             umma_mx8(tmem + m * p.bn, umma_desc_of(low + m * 1024 + 2 * k), umma_desc_of(low + NW * 1024 + 2 * k), idesc,
                      sf + 4 * m, sf + 4 * NW, k ? 1 : accumulate);
         }
-        umma_commit(&bars.empty[at.slot]);
+        umma_commit(empty);
         if ((kb & 3) == 3) umma_commit(&bars.sf_empty[slot]);
       }
       accumulate = 1;
-      at.next(p.stages);
       low = at.slot ? low + (stage_bytes >> 4) : low0;
     }
     if (elect_one()) {
@@ -299,48 +328,56 @@ __global__ void __launch_bounds__(kStreamThreads) fp8_stream_kernel(const __grid
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       joined = true;
     }
-    int parity = 0;
     if (ok) {
       tc_fence_after();
-      const uint32_t feature = (warp & 3) * 32 + lane;
+      const uint32_t feature = 4 * ((warp & 3) * 32 + lane);
       for (int c = 16 * group; c < nt; c += 32) {
-        float v[16], u[16];
-        if (NW == 2) tmem_ld16x2(tmem + quarter + c, tmem + quarter + p.bn + c, v, u);
-        else tmem_ld16(tmem + quarter + c, v);
-        if (splits == 1) {
-          stream_store<NW, 16>(p, bars, v, u, tok0 + c, nt - c, group, parity);
-        } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int q = c / 4 + i;
-            if (q >= quads) break;
-            const uint32_t owner = q % splits;
-            const uint32_t dst = map_cluster_rank(sums, owner) + ((q / splits) * splits + rank) * (NW * 2048) + feature * 16;
-            st_cluster_f4(dst, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            if (NW == 2) st_cluster_f4(dst + 2048, u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+        for (int m = 0; m < NW; ++m) {
+          float v[16];
+          tmem_ld16(tmem + quarter + m * p.bn + c, v);
+          if (splits == 1) {
+            // (over the ring: every load has been read by an MMA, and every MMA has finished)
+            const uint32_t dst = smem_u32(ring) + (c * NW + m) * 512 + feature;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sts_f32(dst + i * (NW * 512), v[i]);
+          } else {
+            int owner = c % splits, slot = c / splits;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (c + i < nt) st_cluster_f32(map_cluster_rank(sums, owner) + ((slot * splits + rank) * NW + m) * 512 + feature, v[i]);
+              if (++owner == splits) owner = 0, ++slot;
+            }
           }
         }
       }
       __syncwarp();
-      if (splits > 1 && lane < min(splits, quads)) mbar_arrive_remote(map_cluster_rank(smem_u32(&bars.sums), lane));
+      if (splits > 1 && lane < min(splits, nt)) mbar_arrive_remote(map_cluster_rank(smem_u32(&bars.sums), lane));
     }
-    if (splits > 1 && mine > 0) {
-      // (an aborted CTA sends nothing: its owners' waits run out, and the status word says so)
-      if (named_bar_and(2, 256, mbar_wait_cluster(&bars.sums, 0, abort_flag, p.err))) {
-        for (int j = group; j < mine; j += 2) {
-          const uint32_t at = sums + j * splits * (NW * 2048) + ((warp & 3) * 32 + lane) * 16;
-          float v[4] = {}, u[4] = {};
-          for (int r = 0; r < splits; ++r) {
-            const float4 a = lds_f4(at + r * (NW * 2048));
-            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-            if (NW == 2) {
-              const float4 b = lds_f4(at + r * (NW * 2048) + 2048);
-              u[0] += b.x, u[1] += b.y, u[2] += b.z, u[3] += b.w;
+    // (an aborted CTA sends nothing: its owners' waits run out, and the status word says so)
+    if (splits == 1) asm volatile("bar.sync 2, 256;" ::: "memory");
+    else if (mine > 0) ok = named_bar_and(2, 256, mbar_wait_cluster(&bars.sums, 0, abort_flag, p.err));
+    if (ok) {
+      const uint32_t src = (splits == 1 ? smem_u32(ring) : sums) + 16 * lane;
+      constexpr int kBatch = 4;  // tokens per warp at a time: their loads and reductions overlap
+      for (int j0 = warp - 2; j0 < mine; j0 += 8 * kBatch) {
+        float4 v[kBatch][NW];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+          for (int m = 0; m < NW; ++m) v[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < splits; ++r) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            if (j0 + 8 * i >= mine) break;
+#pragma unroll
+            for (int m = 0; m < NW; ++m) {
+              const float4 a = lds_f4(src + (((j0 + 8 * i) * splits + r) * NW + m) * 512);
+              v[i][m].x += a.x, v[i][m].y += a.y, v[i][m].z += a.z, v[i][m].w += a.w;
             }
           }
-          const int t = 4 * (rank + j * splits);
-          stream_store<NW, 4>(p, bars, v, u, tok0 + t, nt - t, group, parity);
         }
+        store_tokens<NW, kBatch>(p, v, tok0 + rank + j0 * splits, 8 * splits, (mine - j0 + 7) / 8, row0 + 4 * lane, lane);
       }
     }
     tc_fence_before();
@@ -741,12 +778,11 @@ int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, 
   // its own cluster.
   const uint32_t share = 228 * 1024 / 512 * p.tmem_cols - 1024;
   const uint32_t stage = NW * 16384 + p.bn * 128;
-  const int quads = (p.bn + 3) / 4;
-  const uint32_t fixed = 3072 + (splits > 1 ? (quads + splits - 1) / splits * splits * NW * 2048 : 0);
+  const uint32_t fixed = 2048 + (splits > 1 ? (p.bn + splits - 1) / splits * splits * NW * 512 : 0);
   // two CTAs per SM where there are more than SMs
   const uint32_t budget = ctas * splits > L->sms ? std::max<uint32_t>(share, 113 * 1024) : kSmem;
   p.stages = std::max(1, std::min({kMaxStages, int((budget - fixed) / stage), (p.KB + splits - 1) / splits}));
-  const uint32_t smem = std::max(fixed + p.stages * stage, share);
+  const uint32_t smem = std::max({fixed + p.stages * stage, uint32_t(2048 + NW * p.bn * 512), share});
   if (smem > kSmem) return SCION_EINVAL;
   int st = make_tmap_codes(&p.x, x, T, L->desc.k, p.bn);
   if (st != SCION_OK) return st;
