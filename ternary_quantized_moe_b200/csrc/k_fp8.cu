@@ -34,12 +34,16 @@ typedef __nv_bfloat16 bf16;
 // the token's owner (every warp then arrives on a barrier there), and the owner adds them in rank
 // order.  One barrier of the cluster, at the start, and none on the way out: an owner leaves when
 // everything sent to it has arrived.
-// Roles: warp 0 TMA loads through a ring of 128-column stages, warp 1 the MMAs, warps 2..9 the
+// Roles: warp 0 TMA loads through a ring of stages, warp 1 the MMAs, warps 2..9 the
 // epilogue (two per lane quarter, alternate 16-token chunks), warps 2..5 also the scale words.  The
 // sums pass through shared memory, so that a warp finishes one token at a time with four features
 // per lane: one reduction for a token's scale, 128 features in whole sectors.
 constexpr int kStreamThreads = 320;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 8;
+// K blocks of 128 per stage: waiting for a stage takes as long as four narrow MMAs, so a stage holds
+// eight of them (two blocks of one matrix, or one of two).
+template <int NW>
+constexpr int kStageBlocks = 2 / NW;
 constexpr int kSfSlots = 4;  // ring of scale words, each slot for 4 K blocks (one byte each)
 constexpr uint32_t kNoScale = 0x7f7f7f7fu;  // words of rows past the end: 2^0
 constexpr uint32_t kSmem = 227 * 1024;
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
   const int rank = blockIdx.x, splits = gridDim.x;
   const int row0 = blockIdx.y * 128, tok0 = blockIdx.z * p.bn;
   const int kb0 = int(int64_t(rank) * p.KB / splits), kb1 = int(int64_t(rank + 1) * p.KB / splits);
-  const uint32_t stage_bytes = NW * 16384 + p.bn * 128;
+  const uint32_t block_bytes = NW * 16384 + p.bn * 128, stage_bytes = kStageBlocks<NW> * block_bytes;
   const int nt = min(p.bn, p.T - tok0);
   // this CTA's tokens (rank, rank + splits, ...) and what arrives for them: [token][sender][matrix][feature]
   const int mine = rank < nt ? (nt - rank + splits - 1) / splits : 0;
@@ -220,15 +224,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
     int i = 0;
     uint8_t* st = ring;
     bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb, ++i) {
+    for (int kb = kb0; kb < kb1; kb += kStageBlocks<NW>, ++i) {
       if (i >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[at.slot], at.parity ^ 1, abort_flag, p.err));
       if (!ok) break;
       uint64_t* full = &bars.full[at.slot];
+      const int blocks = min(kStageBlocks<NW>, kb1 - kb);
       if (elect_one()) {
-        mbar_arrive_expect_tx(full, stage_bytes);
-        tma_load_2d(st, &p.w[0], kb * 128, row0, full);
-        if (NW == 2) tma_load_2d(st + 16384, &p.w[1], kb * 128, row0, full);
-        tma_load_2d(st + NW * 16384, &p.x, kb * 128, tok0, full);
+        mbar_arrive_expect_tx(full, blocks * block_bytes);
+        for (int j = 0; j < blocks; ++j) {
+          uint8_t* dst = st + j * block_bytes;
+          tma_load_2d(dst, &p.w[0], (kb + j) * 128, row0, full);
+          if (NW == 2) tma_load_2d(dst + 16384, &p.w[1], (kb + j) * 128, row0, full);
+          tma_load_2d(dst + NW * 16384, &p.x, (kb + j) * 128, tok0, full);
+        }
       }
       at.next(p.stages);
       st = at.slot ? st + stage_bytes : ring;
@@ -238,38 +246,37 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
   } else if (warp == 1) {
     RingPos at;
     bool ok = true;
-    const uint32_t low0 = umma_desc_low(smem_u32(ring));
+    const uint32_t low0 = umma_desc_low(smem_u32(ring)), sf_step = 4 * NW + p.sfb_cols;
     uint32_t low = low0, accumulate = 0;
-    // (the next stage's barrier is tested while the MMAs of this one are issued: a test and the vote on
-    // it take as long as three MMAs of 64 tokens)
-    bool ready = false;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const int slot = (kb >> 2) % kSfSlots;
-      if (kb == kb0 || (kb & 3) == 0) {  // (a slot's phase turns over every four words)
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.sf_full[slot], ((kb >> 2) - (kb0 >> 2)) / kSfSlots & 1, abort_flag, p.err));
-        tc_fence_after();
-      }
-      if (!__all_sync(0xffffffffu, ready))
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
-      if (!ok) break;
-      const uint32_t sf = tmem + p.sf_col + slot * (4 * NW + p.sfb_cols);
-      const uint32_t idesc = umma_idesc_mx8(128, p.bn, kb & 3);
-      uint64_t* empty = &bars.empty[at.slot];
-      at.next(p.stages);
-      ready = mbar_test(&bars.full[at.slot], at.parity);
-      if (elect_one()) {
+    for (int kb = kb0; kb < kb1; kb += kStageBlocks<NW>) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-#pragma unroll
-          for (int m = 0; m < NW; ++m)
-            umma_mx8(tmem + m * p.bn, umma_desc_of(low + m * 1024 + 2 * k), umma_desc_of(low + NW * 1024 + 2 * k), idesc,
-                     sf + 4 * m, sf + 4 * NW, k ? 1 : accumulate);
+      for (int j = 0; j < kStageBlocks<NW>; ++j) {
+        const int b = kb + j, slot = (b >> 2) % kSfSlots;
+        if (b >= kb1) break;
+        if (b == kb0 || (b & 3) == 0) {  // (a slot's phase turns over every four words)
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.sf_full[slot], ((b >> 2) - (kb0 >> 2)) / kSfSlots & 1, abort_flag, p.err));
+          tc_fence_after();
         }
-        umma_commit(empty);
-        if ((kb & 3) == 3) umma_commit(&bars.sf_empty[slot]);
+        if (!ok) break;
+        const uint32_t sf = tmem + p.sf_col + slot * sf_step, idesc = umma_idesc_mx8(128, p.bn, b & 3);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int m = 0; m < NW; ++m)
+              umma_mx8(tmem + m * p.bn, umma_desc_of(low + m * 1024 + 2 * k), umma_desc_of(low + NW * 1024 + 2 * k), idesc,
+                       sf + 4 * m, sf + 4 * NW, k ? 1 : accumulate);
+          }
+          if ((b & 3) == 3) umma_commit(&bars.sf_empty[slot]);
+        }
+        accumulate = 1;
+        low += block_bytes >> 4;
       }
-      accumulate = 1;
-      low = at.slot ? low + (stage_bytes >> 4) : low0;
+      if (!ok) break;
+      if (elect_one()) umma_commit(&bars.empty[at.slot]);
+      at.next(p.stages);
+      if (at.slot == 0) low = low0;
     }
     if (elect_one()) {
       if (ok) umma_commit(&bars.acc_full);
@@ -345,7 +352,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
             int owner = c % splits, slot = c / splits;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              if (c + i < nt) st_cluster_f32(map_cluster_rank(sums, owner) + ((slot * splits + rank) * NW + m) * 512 + feature, v[i]);
+              if (c + i >= nt) break;
+              st_cluster_f32(map_cluster_rank(sums, owner) + ((slot * splits + rank) * NW + m) * 512 + feature, v[i]);
               if (++owner == splits) owner = 0, ++slot;
             }
           }
@@ -777,11 +785,12 @@ int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, 
   // the other too, so no CTA of a cluster can wait for tensor memory held by a CTA that waits for
   // its own cluster.
   const uint32_t share = 228 * 1024 / 512 * p.tmem_cols - 1024;
-  const uint32_t stage = NW * 16384 + p.bn * 128;
+  const uint32_t stage = kStageBlocks<NW> * (NW * 16384 + p.bn * 128);
   const uint32_t fixed = 2048 + (splits > 1 ? (p.bn + splits - 1) / splits * splits * NW * 512 : 0);
   // two CTAs per SM where there are more than SMs
   const uint32_t budget = ctas * splits > L->sms ? std::max<uint32_t>(share, 113 * 1024) : kSmem;
-  p.stages = std::max(1, std::min({kMaxStages, int((budget - fixed) / stage), (p.KB + splits - 1) / splits}));
+  const int range = (p.KB + splits - 1) / splits;  // K blocks of a CTA, at most
+  p.stages = std::max(1, std::min({kMaxStages, int((budget - fixed) / stage), (range + kStageBlocks<NW> - 1) / kStageBlocks<NW>}));
   const uint32_t smem = std::max({fixed + p.stages * stage, uint32_t(2048 + NW * p.bn * 512), share});
   if (smem > kSmem) return SCION_EINVAL;
   int st = make_tmap_codes(&p.x, x, T, L->desc.k, p.bn);
