@@ -90,8 +90,10 @@ __device__ __forceinline__ uint4 scale_round(const uint8_t* row, int r, int KB, 
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Position in a ring of barriers: slot and the parity of its current phase.  (One thread runs each
-// loop over K, so every instruction of its iteration counts: no divisions by the ring's size.)
+// Position in a ring of barriers: slot and the parity of its current phase.  (One warp runs each loop
+// over K, so every instruction of its iteration counts: no divisions by the ring's size, and nothing
+// but straight-line copies, MMAs and commits under elect_one -- with a loop or a branch in there the
+// operands leave the uniform registers and an iteration takes five times as long.)
 struct RingPos {
   int slot = 0;
   uint32_t parity = 0;
@@ -228,14 +230,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
       if (i >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[at.slot], at.parity ^ 1, abort_flag, p.err));
       if (!ok) break;
       uint64_t* full = &bars.full[at.slot];
-      const int blocks = min(kStageBlocks<NW>, kb1 - kb);
+      const bool two = kStageBlocks<NW> == 2 && kb + 1 < kb1;
+      const uint32_t bytes = two ? 2 * block_bytes : block_bytes;
       if (elect_one()) {
-        mbar_arrive_expect_tx(full, blocks * block_bytes);
-        for (int j = 0; j < blocks; ++j) {
-          uint8_t* dst = st + j * block_bytes;
-          tma_load_2d(dst, &p.w[0], (kb + j) * 128, row0, full);
-          if (NW == 2) tma_load_2d(dst + 16384, &p.w[1], (kb + j) * 128, row0, full);
-          tma_load_2d(dst + NW * 16384, &p.x, (kb + j) * 128, tok0, full);
+        mbar_arrive_expect_tx(full, bytes);
+        tma_load_2d(st, &p.w[0], kb * 128, row0, full);
+        if (NW == 2) tma_load_2d(st + 16384, &p.w[1], kb * 128, row0, full);
+        tma_load_2d(st + NW * 16384, &p.x, kb * 128, tok0, full);
+      }
+      if (two) {
+        uint8_t* next = st + block_bytes;
+        if (elect_one()) {
+          tma_load_2d(next, &p.w[0], kb * 128 + 128, row0, full);
+          tma_load_2d(next + NW * 16384, &p.x, kb * 128 + 128, tok0, full);
         }
       }
       at.next(p.stages);
@@ -268,8 +275,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
               umma_mx8(tmem + m * p.bn, umma_desc_of(low + m * 1024 + 2 * k), umma_desc_of(low + NW * 1024 + 2 * k), idesc,
                        sf + 4 * m, sf + 4 * NW, k ? 1 : accumulate);
           }
-          if ((b & 3) == 3) umma_commit(&bars.sf_empty[slot]);
         }
+        if ((b & 3) == 3 && elect_one()) umma_commit(&bars.sf_empty[slot]);
         accumulate = 1;
         low += block_bytes >> 4;
       }
@@ -559,8 +566,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         if (!ok) break;
         const uint32_t st = ring0 + at.slot * kPairStage, full = full0 + 8 * at.slot;
         // both CTAs' copies complete on the first CTA's barrier
+        if (rank == 0 && elect_one()) mbar_arrive_expect_tx(&bars.full[at.slot], 2 * kPairStage);
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&bars.full[at.slot], 2 * kPairStage);
           tma_load_2d_pair(st, &p.x, kb * 128, tok, full);
           tma_load_2d_pair(st + 16384, w, kb * 128, row, full);
         }
@@ -599,10 +606,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
               umma_mx8_pair(tmem, umma_desc_of(low + 2 * k), umma_desc_of(low + 1024 + 2 * k), idesc, sfa, sfa + 4,
                             k ? 1 : kb != 0);
             umma_commit_pair(&bars.empty[at.slot]);
-            if (last) umma_commit_pair(&bars.sf_empty[sf.slot]);
           }
           at.next(kPairStages);
-          if (last) sf.next(kSfSlots);
+          if (last) {
+            if (elect_one()) umma_commit_pair(&bars.sf_empty[sf.slot]);
+            sf.next(kSfSlots);
+          }
         }
         if (ok && elect_one()) umma_commit_pair(&bars.acc_full);
       }
