@@ -4,6 +4,8 @@
 // Both run on tcgen05.mma kind::mxf8f6f4: the tensor cores multiply e4m3 operands and apply the
 // E8M0 scales themselves (a scale byte per row and 32 columns; the four steps of a 128-column block
 // use the same byte), so nothing is expanded or promoted outside them.
+#include <stddef.h>
+
 #include <algorithm>
 #include <new>
 
@@ -185,10 +187,15 @@ __device__ __forceinline__ void store_tokens(const StreamParams& p, float4 (&v)[
 // NW = 1: out = base + W x.  NW = 2: h = silu(W0 x) (W1 x), to bf16 or codes and scales.
 template <int NW>
 __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __grid_constant__ StreamParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  static_assert(sizeof(Bars) <= 1024, "shared memory");
   Bars& bars = *reinterpret_cast<Bars*>(smem);
-  uint8_t* ring = smem + 1024;
+  // 32-bit shared addresses
+  const uint32_t smem0 = smem_u32(smem), ring = smem0 + 1024;
+  const uint32_t full = smem0 + offsetof(Bars, full), empty = smem0 + offsetof(Bars, empty);
+  const uint32_t sf_full = smem0 + offsetof(Bars, sf_full), sf_empty = smem0 + offsetof(Bars, sf_empty);
+  const uint32_t acc_full = smem0 + offsetof(Bars, acc_full), done = smem0 + offsetof(Bars, done);
+  const uint32_t sums_full = smem0 + offsetof(Bars, sums);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x, splits = gridDim.x;
   const int row0 = blockIdx.y * 128, tok0 = blockIdx.z * p.bn;
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
   const int nt = min(p.bn, p.T - tok0);
   // this CTA's tokens (rank, rank + splits, ...) and what arrives for them: [token][sender][matrix][feature]
   const int mine = rank < nt ? (nt - rank + splits - 1) / splits : 0;
-  const uint32_t sums = smem_u32(ring + p.stages * stage_bytes);
+  const uint32_t sums = ring + p.stages * stage_bytes;
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&p.w[0]), tma_prefetch_map(&p.x);
@@ -224,45 +231,45 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
   if (warp == 0) {
     RingPos at;
     int i = 0;
-    uint8_t* st = ring;
+    uint32_t st = ring;
     bool ok = true;
     for (int kb = kb0; kb < kb1; kb += kStageBlocks<NW>, ++i) {
-      if (i >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[at.slot], at.parity ^ 1, abort_flag, p.err));
+      if (i >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * at.slot, at.parity ^ 1, abort_flag, p.err));
       if (!ok) break;
-      uint64_t* full = &bars.full[at.slot];
+      const uint32_t bar = full + 8 * at.slot;
       const bool two = kStageBlocks<NW> == 2 && kb + 1 < kb1;
       const uint32_t bytes = two ? 2 * block_bytes : block_bytes;
       if (elect_one()) {
-        mbar_arrive_expect_tx(full, bytes);
-        tma_load_2d(st, &p.w[0], kb * 128, row0, full);
-        if (NW == 2) tma_load_2d(st + 16384, &p.w[1], kb * 128, row0, full);
-        tma_load_2d(st + NW * 16384, &p.x, kb * 128, tok0, full);
+        mbar_arrive_expect_tx(bar, bytes);
+        tma_load_2d(st, &p.w[0], kb * 128, row0, bar);
+        if (NW == 2) tma_load_2d(st + 16384, &p.w[1], kb * 128, row0, bar);
+        tma_load_2d(st + NW * 16384, &p.x, kb * 128, tok0, bar);
       }
       if (two) {
-        uint8_t* next = st + block_bytes;
+        const uint32_t next = st + block_bytes;
         if (elect_one()) {
-          tma_load_2d(next, &p.w[0], kb * 128 + 128, row0, full);
-          tma_load_2d(next + NW * 16384, &p.x, kb * 128 + 128, tok0, full);
+          tma_load_2d(next, &p.w[0], kb * 128 + 128, row0, bar);
+          tma_load_2d(next + NW * 16384, &p.x, kb * 128 + 128, tok0, bar);
         }
       }
       at.next(p.stages);
       st = at.slot ? st + stage_bytes : ring;
     }
     // copies may still be in flight if the MMA warp gave up
-    for (int j = max(0, i - p.stages); j < i; ++j) mbar_drain(&bars.full[j % p.stages], (j / p.stages) & 1);
+    for (int j = max(0, i - p.stages); j < i; ++j) mbar_drain(full + 8 * (j % p.stages), (j / p.stages) & 1);
   } else if (warp == 1) {
     RingPos at;
     bool ok = true;
-    const uint32_t low0 = umma_desc_low(smem_u32(ring)), sf_step = 4 * NW + p.sfb_cols;
+    const uint32_t low0 = umma_desc_low(ring), sf_step = 4 * NW + p.sfb_cols;
     uint32_t low = low0, accumulate = 0;
     for (int kb = kb0; kb < kb1; kb += kStageBlocks<NW>) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
+      ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * at.slot, at.parity, abort_flag, p.err));
 #pragma unroll
       for (int j = 0; j < kStageBlocks<NW>; ++j) {
         const int b = kb + j, slot = (b >> 2) % kSfSlots;
         if (b >= kb1) break;
         if (b == kb0 || (b & 3) == 0) {  // (a slot's phase turns over every four words)
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.sf_full[slot], ((b >> 2) - (kb0 >> 2)) / kSfSlots & 1, abort_flag, p.err));
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(sf_full + 8 * slot, ((b >> 2) - (kb0 >> 2)) / kSfSlots & 1, abort_flag, p.err));
           tc_fence_after();
         }
         if (!ok) break;
@@ -276,21 +283,21 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
                        sf + 4 * m, sf + 4 * NW, k ? 1 : accumulate);
           }
         }
-        if ((b & 3) == 3 && elect_one()) umma_commit(&bars.sf_empty[slot]);
+        if ((b & 3) == 3 && elect_one()) umma_commit(sf_empty + 8 * slot);
         accumulate = 1;
         low += block_bytes >> 4;
       }
       if (!ok) break;
-      if (elect_one()) umma_commit(&bars.empty[at.slot]);
+      if (elect_one()) umma_commit(empty + 8 * at.slot);
       at.next(p.stages);
       if (at.slot == 0) low = low0;
     }
     if (elect_one()) {
-      if (ok) umma_commit(&bars.acc_full);
-      umma_commit(&bars.done);
+      if (ok) umma_commit(acc_full);
+      umma_commit(done);
     }
     // every MMA issued above has finished before tensor memory is released
-    mbar_drain(&bars.done, 0);
+    mbar_drain(done, 0);
   } else {
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
     const int group = (warp - 2) >> 2;
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
           const int q = 4 * r + slot, i = q - q0;
           if (i < 0 || q > q1) continue;
           if (i >= kSfSlots) {
-            ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (i / kSfSlots - 1) & 1, abort_flag, p.err));
+            ok = named_bar_and(1, 128, mbar_wait(sf_empty + 8 * slot, (i / kSfSlots - 1) & 1, abort_flag, p.err));
             if (!ok) break;
             tc_fence_after();
           }
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
         if (r < q1 / 4) load(r + 1);
       }
     }
-    ok = named_bar_and(2, 256, ok && mbar_wait(&bars.acc_full, 0, abort_flag, p.err));
+    ok = named_bar_and(2, 256, ok && mbar_wait(acc_full, 0, abort_flag, p.err));
     if (splits > 1) {
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       joined = true;
@@ -352,7 +359,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
           tmem_ld16(tmem + quarter + m * p.bn + c, v);
           if (splits == 1) {
             // (over the ring: every load has been read by an MMA, and every MMA has finished)
-            const uint32_t dst = smem_u32(ring) + (c * NW + m) * 512 + feature;
+            const uint32_t dst = ring + (c * NW + m) * 512 + feature;
 #pragma unroll
             for (int i = 0; i < 16; ++i) sts_f32(dst + i * (NW * 512), v[i]);
           } else {
@@ -367,13 +374,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
         }
       }
       __syncwarp();
-      if (splits > 1 && lane < min(splits, nt)) mbar_arrive_remote(map_cluster_rank(smem_u32(&bars.sums), lane));
+      if (splits > 1 && lane < min(splits, nt)) mbar_arrive_remote(map_cluster_rank(sums_full, lane));
     }
     // (an aborted CTA sends nothing: its owners' waits run out, and the status word says so)
     if (splits == 1) asm volatile("bar.sync 2, 256;" ::: "memory");
-    else if (mine > 0) ok = named_bar_and(2, 256, mbar_wait_cluster(&bars.sums, 0, abort_flag, p.err));
+    else if (mine > 0) ok = named_bar_and(2, 256, mbar_wait_cluster(sums_full, 0, abort_flag, p.err));
     if (ok) {
-      const uint32_t src = (splits == 1 ? smem_u32(ring) : sums) + 16 * lane;
+      const uint32_t src = (splits == 1 ? ring : sums) + 16 * lane;
       constexpr int kBatch = 4;  // tokens per warp at a time: their loads and reductions overlap
       for (int j0 = warp - 2; j0 < mine; j0 += 8 * kBatch) {
         float4 v[kBatch][NW];
@@ -523,8 +530,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   constexpr bool kGated = EPI == kPairGatedBf16 || EPI == kPairGatedCodes;
   extern __shared__ __align__(1024) uint8_t smem[];
   static_assert(kPairStages * kPairStage + 32768 + sizeof(PairBars) <= kSmem, "shared memory");
-  uint8_t* ring = smem;
-  const uint32_t staging = smem_u32(ring) + kPairStages * kPairStage;
+  // 32-bit shared addresses
+  const uint32_t ring = smem_u32(smem), staging = ring + kPairStages * kPairStage, bar0 = staging + 32768;
+  const uint32_t full = bar0 + offsetof(PairBars, full), empty = bar0 + offsetof(PairBars, empty);
+  const uint32_t sf_full = bar0 + offsetof(PairBars, sf_full), sf_empty = bar0 + offsetof(PairBars, sf_empty);
+  const uint32_t acc_full = bar0 + offsetof(PairBars, acc_full), acc_empty = bar0 + offsetof(PairBars, acc_empty);
+  const uint32_t done = bar0 + offsetof(PairBars, done);
   PairBars& bars = *reinterpret_cast<PairBars*>(smem + kPairStages * kPairStage + 32768);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     RingPos at;
     int i = 0;
     bool ok = true;
-    const uint32_t ring0 = smem_u32(ring), full0 = map_cluster_rank(smem_u32(&bars.full[0]), 0);
+    const uint32_t full0 = map_cluster_rank(full, 0);
     for (int tile = pair; tile < n_tiles && ok; tile += pairs) {
       int mt, nt;
       pair_tile(p, tile, mt, nt);
@@ -562,20 +573,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       const CUtensorMap* w = &p.w[kGated ? rank : 0];
       for (int kb = 0; kb < p.KB; ++kb, ++i) {
         if (i >= kPairStages)
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[at.slot], at.parity ^ 1, abort_flag, p.err));
+          ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * at.slot, at.parity ^ 1, abort_flag, p.err));
         if (!ok) break;
-        const uint32_t st = ring0 + at.slot * kPairStage, full = full0 + 8 * at.slot;
+        const uint32_t st = ring + at.slot * kPairStage, bar = full0 + 8 * at.slot;
         // both CTAs' copies complete on the first CTA's barrier
-        if (rank == 0 && elect_one()) mbar_arrive_expect_tx(&bars.full[at.slot], 2 * kPairStage);
+        if (rank == 0 && elect_one()) mbar_arrive_expect_tx(full + 8 * at.slot, 2 * kPairStage);
         if (elect_one()) {
-          tma_load_2d_pair(st, &p.x, kb * 128, tok, full);
-          tma_load_2d_pair(st + 16384, w, kb * 128, row, full);
+          tma_load_2d_pair(st, &p.x, kb * 128, tok, bar);
+          tma_load_2d_pair(st + 16384, w, kb * 128, row, bar);
         }
         at.next(kPairStages);
       }
     }
     if (rank == 0) {
-      for (int j = max(0, i - kPairStages); j < i; ++j) mbar_drain(&bars.full[j % kPairStages], (j / kPairStages) & 1);
+      for (int j = max(0, i - kPairStages); j < i; ++j) mbar_drain(full + 8 * (j % kPairStages), (j / kPairStages) & 1);
     } else if (!ok) {
       // given up: the copies complete on the other CTA's barrier; leave them time to land
       for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
@@ -586,15 +597,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       RingPos at, sf;
       uint32_t acc_parity = 1;
       bool ok = true;
-      const uint32_t low0 = umma_desc_low(smem_u32(ring));
+      const uint32_t low0 = umma_desc_low(ring);
       for (int tile = pair; tile < n_tiles && ok; tile += pairs, acc_parity ^= 1) {
-        if (tile != pair) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bars.acc_empty, acc_parity, abort_flag, p.err));
+        if (tile != pair) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_empty, acc_parity, abort_flag, p.err));
         for (int kb = 0; kb < p.KB && ok; ++kb) {
           if ((kb & 3) == 0) {
-            ok = mbar_wait_cluster(&bars.sf_full[sf.slot], sf.parity, abort_flag, p.err);
+            ok = mbar_wait_cluster(sf_full + 8 * sf.slot, sf.parity, abort_flag, p.err);
             tc_fence_after();
           }
-          ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.full[at.slot], at.parity, abort_flag, p.err));
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(full + 8 * at.slot, at.parity, abort_flag, p.err));
           if (!ok) break;
           const uint32_t low = low0 + at.slot * (kPairStage >> 4);
           const uint32_t sfa = tmem + kPairSfCol + sf.slot * 12;
@@ -605,20 +616,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             for (int k = 0; k < 4; ++k)
               umma_mx8_pair(tmem, umma_desc_of(low + 2 * k), umma_desc_of(low + 1024 + 2 * k), idesc, sfa, sfa + 4,
                             k ? 1 : kb != 0);
-            umma_commit_pair(&bars.empty[at.slot]);
+            umma_commit_pair(empty + 8 * at.slot);
           }
           at.next(kPairStages);
           if (last) {
-            if (elect_one()) umma_commit_pair(&bars.sf_empty[sf.slot]);
+            if (elect_one()) umma_commit_pair(sf_empty + 8 * sf.slot);
             sf.next(kSfSlots);
           }
         }
-        if (ok && elect_one()) umma_commit_pair(&bars.acc_full);
+        if (ok && elect_one()) umma_commit_pair(acc_full);
       }
-      if (elect_one()) umma_commit_pair(&bars.done);
+      if (elect_one()) umma_commit_pair(done);
     }
     // the last arrival of a commit on either CTA's barriers
-    mbar_drain(&bars.done, 0);
+    mbar_drain(done, 0);
   } else if (warp < 4) {
   } else if (warp < 8) {
     regs_down<48>();
@@ -650,7 +661,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
           if (q + i >= nq) break;
           const int slot = sq % kSfSlots;
           if (sq >= kSfSlots) {
-            ok = named_bar_and(1, 128, mbar_wait(&bars.sf_empty[slot], (sq / kSfSlots - 1) & 1, abort_flag, p.err));
+            ok = named_bar_and(1, 128, mbar_wait(sf_empty + 8 * slot, (sq / kSfSlots - 1) & 1, abort_flag, p.err));
             if (!ok) break;
             tc_fence_after();
           }
@@ -662,7 +673,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(map_cluster_rank(smem_u32(&bars.sf_full[slot]), 0));
+          if (lane == 0) mbar_arrive_remote(map_cluster_rank(sf_full + 8 * slot, 0));
           ++sq;
         }
         // the next round, or the first of the next tile
@@ -677,7 +688,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     // plain: 128 consecutive columns; gated: 64 gate columns and the up columns of the same features
     const uint32_t acc0 = tmem + (uint32_t(quarter * 32) << 16) + half * (kGated ? 64 : 128);
     const uint32_t acc1 = acc0 + (kGated ? 128 : 64);
-    const uint32_t released = map_cluster_rank(smem_u32(&bars.acc_empty), 0);
+    const uint32_t released = map_cluster_rank(acc_empty, 0);
     uint32_t parity = 0;
     for (int tile = pair; tile < n_tiles; tile += pairs, parity ^= 1) {
       int mt, nt;
@@ -686,7 +697,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
                          nt * 256 + half * 128, p.T, p.N, p.out_bf16};
       float4 base[8];
       load_base<EPI == kPairBase>(rows, 0, lane, base);  // (in flight during the tile's MMAs)
-      if (!named_bar_and(2, 256, mbar_wait(&bars.acc_full, parity, abort_flag, p.err))) break;
+      if (!named_bar_and(2, 256, mbar_wait(acc_full, parity, abort_flag, p.err))) break;
       tc_fence_after();
       uint32_t v[128];
       tmem_ld64x2(acc0, acc1, v);
