@@ -4,10 +4,29 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace scion {
 namespace fp8 {
+
+// One product call: out = base + W x (w[1] null), or h = silu(W0 x) (W1 x) to bf16 or codes and scales.
+struct Call {
+  const uint8_t* x;
+  const uint8_t* sx;
+  const uint8_t* w[2];
+  const uint8_t* sw[2];
+  const float* base;
+  void* out;  // plain: out; gated: bf16 h or null
+  uint8_t* codes;
+  uint8_t* scales;
+  int T, N, K, KB;  // KB = ceil(K / 128)
+  int out_bf16;
+};
+
+// k_fp8_rows.cu: few tokens
+constexpr int kRowsTokens = 16;
+cudaError_t launch_rows(const Call& c, cudaStream_t s);
 
 // |v| as an unsigned integer: ordered like the magnitudes, infinities and NaN above every number
 // (a maximum over these keeps a NaN, which fmaxf would drop).
@@ -31,6 +50,8 @@ __device__ __forceinline__ float scale_inverse(uint32_t b) {
 __device__ __forceinline__ float scale_value(uint32_t b) {
   return b == 255u ? __uint_as_float(0x7fffffffu) : b ? __uint_as_float(b << 23) : __uint_as_float(0x00400000u);
 }
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
 // Four values (already times scale_inverse) to four e4m3 bytes, the first in the lowest byte.
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {

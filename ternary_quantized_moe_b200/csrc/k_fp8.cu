@@ -109,8 +109,6 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
-
 // The results of `count` (at most B) tokens t, t + step, ...: features n .. n + 3 of this lane.
 template <int NW, int B>
 __device__ __forceinline__ void store_tokens(const StreamParams& p, float4 (&v)[B][NW], int t, int step, int count, int n,
@@ -840,6 +838,14 @@ int launch_pair(const scion_fp8* L, const StreamParams& q, const uint8_t* x, int
   return status(launch_pdl_cluster(fp8_pair_kernel<EPI>, dim3(2 * pairs), dim3(kPairThreads), dim3(2, 1, 1), kSmem, s, p));
 }
 
+Call call(const scion_fp8* L, const uint8_t* x, const uint8_t* sx, int T) {
+  Call c{};
+  c.x = x, c.sx = sx;
+  c.w[0] = L->desc.w_codes, c.sw[0] = L->desc.w_scales, c.w[1] = L->desc.up_codes, c.sw[1] = L->desc.up_scales;
+  c.T = T, c.N = L->desc.n, c.K = L->desc.k, c.KB = (c.K + 127) / 128;
+  return c;
+}
+
 StreamParams params(const scion_fp8* L, const uint8_t* sx, int T) {
   StreamParams p{};
   p.sx = sx, p.sw[0] = L->desc.w_scales, p.sw[1] = L->desc.up_scales;
@@ -907,10 +913,15 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
   if (!x_codes || !x_scales || !out || scion::misaligned(x_codes, 16)) return SCION_EINVAL;
   if (scion::misaligned(base, 4) || scion::misaligned(out, out_type == SCION_F32 ? 4 : 2)) return SCION_EINVAL;
   if (out_type == SCION_BF16 && static_cast<const void*>(base) == out && base) return SCION_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T <= scion::fp8::kRowsTokens) {
+    scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);
+    c.base = base, c.out = out, c.out_bf16 = out_type == SCION_BF16;
+    return scion::status(scion::fp8::launch_rows(c, s));
+  }
   scion::StreamParams p = scion::params(L, x_scales, T);
   p.base = base, p.out = out, p.out_bf16 = out_type == SCION_BF16;
   p.vec = p.N % 4 == 0 && !scion::misaligned(base, 16) && !scion::misaligned(out, 16);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool rows16 = int64_t(p.N) * (p.out_bf16 ? 2 : 4) % 16 == 0 && p.vec;
   if (scion::use_pair(L, T, rows16))
     return base         ? scion::launch_pair<scion::kPairBase>(L, p, x_codes, T, s)
@@ -927,9 +938,14 @@ extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_
   if (!x_codes || !x_scales || scion::misaligned(x_codes, 16) || scion::misaligned(h_bf16, 16) ||
       scion::misaligned(h_codes, 16))
     return SCION_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T <= scion::fp8::kRowsTokens) {
+    scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);
+    c.out = h_bf16, c.codes = h_codes, c.scales = h_scales;
+    return scion::status(scion::fp8::launch_rows(c, s));
+  }
   scion::StreamParams p = scion::params(L, x_scales, T);
   p.out = h_bf16, p.codes = h_codes, p.scales = h_scales;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (scion::use_pair(L, T, true))
     return h_codes ? scion::launch_pair<scion::kPairGatedCodes>(L, p, x_codes, T, s)
                    : scion::launch_pair<scion::kPairGatedBf16>(L, p, x_codes, T, s);

@@ -1,0 +1,170 @@
+// k_fp8_rows.cu -- products in e4m3 with power-of-two block scales for single tokens and small decode
+// batches (up to 16 tokens).
+//
+// Bound by latency and by reading the weights once, so the path from the first load to the result is
+// kept short: no ring, no tensor memory, no cluster for a plain layer.  A CTA holds 16 weight rows (of
+// each matrix) and its eight warps split K by blocks of 128; a lane loads its share of a block straight
+// into mma.sync fragments.  The order of k inside a block is free as long as both operands agree, so a
+// lane takes 32 consecutive bytes of its row -- four lanes cover the row's 128 bytes -- and step s of
+// the four uses bytes 8 s .. 8 s + 7 of them.  A block's sum is scaled once (both scales are powers of
+// two) and added in fp32; the warps' sums meet in shared memory and are added in warp order.
+// A gated layer that writes 8 bits needs the largest |h| of 128 features: the eight CTAs of a cluster
+// hold them and exchange one magnitude per token.
+#include "fp8_common.cuh"
+#include "scion_internal.cuh"
+
+namespace scion {
+namespace {
+
+using namespace fp8;
+typedef __nv_bfloat16 bf16;
+
+constexpr int kRowsWarps = 8;
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct Bytes32 {
+  uint4 v[2];
+};
+// 32 bytes at p (16-byte aligned); `n` of them exist (a multiple of 16, or less than 1), the rest are 0.
+__device__ __forceinline__ Bytes32 load32(const uint8_t* p, int n) {
+  Bytes32 b;
+  b.v[0] = b.v[1] = make_uint4(0u, 0u, 0u, 0u);
+  if (n > 0) b.v[0] = *reinterpret_cast<const uint4*>(p);
+  if (n > 16) b.v[1] = *reinterpret_cast<const uint4*>(p + 16);
+  return b;
+}
+__device__ __forceinline__ uint32_t word(const Bytes32& b, int i) {
+  const uint4& v = b.v[i >> 2];
+  return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+}
+
+// acc + v 2^(a - 127) 2^(b - 127) for scale bytes a and b, as two factors of the same sign of exponent,
+// so that nothing between overflows or underflows where the result does not.
+__device__ __forceinline__ float add_scaled(float acc, float v, uint32_t a, uint32_t b) {
+  const int e = int(a + b) - 254, e1 = e >> 1, e2 = e - e1;
+  const float f1 = __uint_as_float(uint32_t(e1 + 127) << 23), f2 = __uint_as_float(uint32_t(e2 + 127) << 23);
+  return (a == 255u || b == 255u) ? NAN : fmaf(v * f1, f2, acc);
+}
+
+// NW matrices, NT tiles of 8 tokens, G: results to 8 bits (gated, clusters of 8 CTAs)
+template <int NW, int NT, bool G>
+__global__ void __launch_bounds__(kRowsWarps * 32, 2) fp8_rows_kernel(const Call p) {
+  __shared__ float part[kRowsWarps][NW][8 * NT][17];  // [warp][matrix][token][row], padded
+  __shared__ uint32_t amax[8][8 * NT];                // [CTA of the cluster][token]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int row0 = blockIdx.x * 16;
+  pdl_trigger();
+  pdl_wait();
+  float acc[NW][NT][4] = {};
+  if (row0 < p.N) {  // (a cluster's last CTAs may have no rows)
+#pragma unroll 2
+    for (int kb = warp; kb < p.KB; kb += kRowsWarps) {
+      const int k = kb * 128 + 32 * c, left = p.K - k;
+      Bytes32 w[NW][2], x[NT];
+      uint32_t sw[NW], sx[NT][2];
+#pragma unroll
+      for (int m = 0; m < NW; ++m) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = row0 + g + 8 * h;
+          w[m][h] = load32(p.w[m] + int64_t(r) * p.K + k, r < p.N ? left : 0);
+        }
+        sw[m] = p.sw[m][int64_t(row0 / 128) * p.KB + kb];
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        x[t] = load32(p.x + int64_t(8 * t + g) * p.K + k, 8 * t + g < p.T ? left : 0);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int tok = 8 * t + 2 * c + j;
+          sx[t][j] = tok < p.T ? p.sx[int64_t(tok) * p.KB + kb] : 127u;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < NW; ++m) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            mma_e4m3(d, word(w[m][0], 2 * s), word(w[m][1], 2 * s), word(w[m][0], 2 * s + 1), word(w[m][1], 2 * s + 1),
+                     word(x[t], 2 * s), word(x[t], 2 * s + 1));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][t][i] = add_scaled(acc[m][t][i], d[i], sx[t][i & 1], sw[m]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < NW; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[warp][m][8 * t + 2 * c + (i & 1)][g + 8 * (i >> 1)] = acc[m][t][i];
+  __syncthreads();
+  // thread: row threadIdx % 16 of token threadIdx / 16 (a half warp per token)
+  const int r = threadIdx.x & 15, tok = threadIdx.x >> 4, n = row0 + r;
+  const bool mine = tok < 8 * NT && tok < p.T && n < p.N;
+  float v[NW];
+#pragma unroll
+  for (int m = 0; m < NW; ++m) {
+    v[m] = 0.f;
+    if (tok < 8 * NT)
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) v[m] += part[w][m][tok][r];
+  }
+  const int64_t at = int64_t(tok) * p.N + n;
+  if (NW == 1) {
+    if (!mine) return;
+    if (p.base) v[0] += p.base[at];
+    if (p.out_bf16) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(v[0]);
+    else static_cast<float*>(p.out)[at] = v[0];
+    return;
+  }
+  const float h = silu_mul(v[0], v[NW - 1]);
+  if (!G) {
+    if (mine) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(h);
+    return;
+  }
+  const uint32_t half = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
+  const uint32_t m = __reduce_max_sync(half, mine ? mag(h) : 0u);
+  const int rank = blockIdx.x & 7;
+  if (tok < 8 * NT && r < 8) {  // one magnitude per token to each CTA of the cluster
+    const uint32_t dst = map_cluster_rank(smem_addr(&amax[rank][tok]), r);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst), "r"(m) : "memory");
+  }
+  cluster_sync();
+  if (!mine) return;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, amax[i][tok]);
+  const uint32_t b = scale_byte(top);
+  p.codes[at] = uint8_t(pack4(h * scale_inverse(b), 0.f, 0.f, 0.f));
+  if (rank == 0 && r == 0) p.scales[int64_t(tok) * ((p.N + 127) / 128) + (blockIdx.x >> 3)] = uint8_t(b);
+}
+
+template <int NW, int NT, bool G>
+cudaError_t launch(const Call& c, cudaStream_t s) {
+  const unsigned ctas = unsigned((c.N + 15) / 16);
+  const dim3 block(kRowsWarps * 32);
+  if (G) return launch_pdl_cluster(fp8_rows_kernel<NW, NT, G>, dim3((ctas + 7) / 8 * 8), block, dim3(8), 0, s, c);
+  return launch_pdl(fp8_rows_kernel<NW, NT, G>, dim3(ctas), block, 0, s, c);
+}
+
+}  // namespace
+
+namespace fp8 {
+cudaError_t launch_rows(const Call& c, cudaStream_t s) {
+  if (!c.w[1]) return c.T <= 8 ? launch<1, 1, false>(c, s) : launch<1, 2, false>(c, s);
+  if (!c.codes) return c.T <= 8 ? launch<2, 1, false>(c, s) : launch<2, 2, false>(c, s);
+  return c.T <= 8 ? launch<2, 1, true>(c, s) : launch<2, 2, true>(c, s);
+}
+}  // namespace fp8
+}  // namespace scion
