@@ -24,8 +24,7 @@ struct Call {
   int out_bf16;
 };
 
-// k_fp8_rows.cu: few tokens
-constexpr int kRowsTokens = 16;
+// k_fp8_rows.cu: up to 16 tokens
 cudaError_t launch_rows(const Call& c, cudaStream_t s);
 
 // |v| as an unsigned integer: ordered like the magnitudes, infinities and NaN above every number

@@ -17,7 +17,8 @@ struct scion_fp8 {
   scion_fp8_desc desc;
   CUtensorMap w[2];
   int sms;
-  int* err;  // device status word
+  int clusters[9];  // clusters of 1 .. 8 CTAs that run at once with one CTA per SM
+  int* err;         // device status word
   size_t device_bytes;
 };
 
@@ -783,6 +784,17 @@ int status(cudaError_t e) {
   return e == cudaSuccess ? SCION_OK : e == cudaErrorMemoryAllocation ? SCION_ENOMEM : SCION_ECUDA;
 }
 
+// Clusters of n CTAs of the stream kernel that are on the current device at once, one CTA per SM.
+cudaError_t max_clusters(int n, int* count) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n), cfg.blockDim = dim3(kStreamThreads), cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = n, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr, cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(count, fp8_stream_kernel<1>, &cfg);
+}
+
 template <int NW>
 int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, cudaStream_t s) {
   p.w[0] = L->w[0], p.w[1] = L->w[NW - 1];
@@ -794,8 +806,11 @@ int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, 
   const int t_tiles = (T + most - 1) / most;
   p.bn = ((T + t_tiles - 1) / t_tiles + 15) / 16 * 16;
   const int ctas = n_tiles * t_tiles;
-  // (the sums of a wide tile would leave too little shared memory for the ring)
-  const int splits = p.bn > 128 / NW ? 1 : std::max(1, std::min({8, p.KB, L->sms / ctas}));
+  // as many CTAs per tile as run at once (the sums of a wide tile would leave too little shared memory
+  // for the ring).  16 tiles of 64 tokens, K = 4096: 7.8 us with clusters of 6, 13.5 with clusters of 8,
+  // of which 15 fit.
+  int splits = p.bn > 128 / NW ? 1 : std::min(8, p.KB);
+  while (splits > 1 && L->clusters[splits] < ctas) --splits;
   p.sfb_cols = p.bn > 128 ? 8 : 4;
   p.sf_col = NW * p.bn;
   p.tmem_cols = int(tmem_cols_pow2(p.sf_col + kSfSlots * (4 * NW + p.sfb_cols)));
@@ -815,6 +830,13 @@ int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, 
   if (st != SCION_OK) return st;
   return status(launch_pdl_cluster(fp8_stream_kernel<NW>, dim3(splits, n_tiles, t_tiles), dim3(kStreamThreads),
                                    dim3(splits, 1, 1), smem, s, p));
+}
+
+// Up to 8 tokens, and up to 16 with few weights, run on mma.sync (k_fp8_rows.cu): it starts sooner, but
+// reads the tokens again for every 16 weight rows.  1 token, 8 MB of weights: 2.9 us against 5.2; 16
+// tokens: 8 MB 4.0 against 6.1, 22 MB 11.0 against 8.5, 67 MB 22.8 against 15.3.
+bool use_rows(const Call& c) {
+  return c.T <= 8 || (c.T <= 16 && int64_t(c.N) * c.K * (c.w[1] ? 2 : 1) <= (12 << 20));
 }
 
 // The pair kernel where its tiles fill the SMs and rows can be stored in 16-byte pieces.
@@ -886,6 +908,7 @@ extern "C" int scion_fp8_create(const scion_fp8_desc* D, void* stream, scion_fp8
   for (const auto f : {scion::fp8_pair_kernel<scion::kPairBf16>, scion::fp8_pair_kernel<scion::kPairF32>,
                        scion::fp8_pair_kernel<scion::kPairBase>, scion::fp8_pair_kernel<scion::kPairGatedBf16>, scion::fp8_pair_kernel<scion::kPairGatedCodes>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, scion::kSmem);
+  for (int n = 1; n <= 8 && e == cudaSuccess; ++n) e = scion::max_clusters(n, &L->clusters[n]);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&L->err), sizeof(int));
   if (e == cudaSuccess) e = cudaMemsetAsync(L->err, 0, sizeof(int), static_cast<cudaStream_t>(stream));
   // (the word is cleared before a forward on another stream can run)
@@ -914,11 +937,9 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
   if (scion::misaligned(base, 4) || scion::misaligned(out, out_type == SCION_F32 ? 4 : 2)) return SCION_EINVAL;
   if (out_type == SCION_BF16 && static_cast<const void*>(base) == out && base) return SCION_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T <= scion::fp8::kRowsTokens) {
-    scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);
-    c.base = base, c.out = out, c.out_bf16 = out_type == SCION_BF16;
-    return scion::status(scion::fp8::launch_rows(c, s));
-  }
+  scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);
+  c.base = base, c.out = out, c.out_bf16 = out_type == SCION_BF16;
+  if (scion::use_rows(c)) return scion::status(scion::fp8::launch_rows(c, s));
   scion::StreamParams p = scion::params(L, x_scales, T);
   p.base = base, p.out = out, p.out_bf16 = out_type == SCION_BF16;
   p.vec = p.N % 4 == 0 && !scion::misaligned(base, 16) && !scion::misaligned(out, 16);
@@ -939,11 +960,9 @@ extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_
       scion::misaligned(h_codes, 16))
     return SCION_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T <= scion::fp8::kRowsTokens) {
-    scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);
-    c.out = h_bf16, c.codes = h_codes, c.scales = h_scales;
-    return scion::status(scion::fp8::launch_rows(c, s));
-  }
+  scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);
+  c.out = h_bf16, c.codes = h_codes, c.scales = h_scales;
+  if (scion::use_rows(c)) return scion::status(scion::fp8::launch_rows(c, s));
   scion::StreamParams p = scion::params(L, x_scales, T);
   p.out = h_bf16, p.codes = h_codes, p.scales = h_scales;
   if (scion::use_pair(L, T, true))

@@ -53,8 +53,9 @@ __device__ __forceinline__ float add_scaled(float acc, float v, uint32_t a, uint
   return (a == 255u || b == 255u) ? NAN : fmaf(v * f1, f2, acc);
 }
 
-// NW matrices, NT tiles of 8 tokens, G: results to 8 bits (gated, clusters of 8 CTAs)
-template <int NW, int NT, bool G>
+// NW matrices, NT tiles of 8 tokens, U blocks of K per warp with their loads in flight together, G:
+// results to 8 bits (gated, clusters of 8 CTAs)
+template <int NW, int NT, int U, bool G>
 __global__ void __launch_bounds__(kRowsWarps * 32, 2) fp8_rows_kernel(const Call p) {
   __shared__ float part[kRowsWarps][NW][8 * NT][17];  // [warp][matrix][token][row], padded
   __shared__ uint32_t amax[8][8 * NT];                // [CTA of the cluster][token]
@@ -63,30 +64,40 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 2) fp8_rows_kernel(const Call
   pdl_trigger();
   pdl_wait();
   float acc[NW][NT][4] = {};
-  if (row0 < p.N) {  // (a cluster's last CTAs may have no rows)
-#pragma unroll 2
-    for (int kb = warp; kb < p.KB; kb += kRowsWarps) {
-      const int k = kb * 128 + 32 * c, left = p.K - k;
-      Bytes32 w[NW][2], x[NT];
-      uint32_t sw[NW], sx[NT][2];
+  // (a cluster's last CTAs may have no rows)
+  for (int kb0 = warp; kb0 < p.KB && row0 < p.N; kb0 += kRowsWarps * U) {
+    Bytes32 w[U][NW][2], x[U][NT];
+    uint32_t sw[U][NW], sx[U][NT][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = kb0 + u * kRowsWarps, k = kb * 128 + 32 * c, left = p.K - k;  // (left < 1 past the end)
 #pragma unroll
       for (int m = 0; m < NW; ++m) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = row0 + g + 8 * h;
-          w[m][h] = load32(p.w[m] + int64_t(r) * p.K + k, r < p.N ? left : 0);
+          w[u][m][h] = load32(p.w[m] + int64_t(r) * p.K + k, r < p.N ? left : 0);
         }
-        sw[m] = p.sw[m][int64_t(row0 / 128) * p.KB + kb];
       }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = kb0 + u * kRowsWarps, k = kb * 128 + 32 * c, left = p.K - k;
+      const bool in = kb < p.KB;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        x[t] = load32(p.x + int64_t(8 * t + g) * p.K + k, 8 * t + g < p.T ? left : 0);
+        x[u][t] = load32(p.x + int64_t(8 * t + g) * p.K + k, 8 * t + g < p.T ? left : 0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int tok = 8 * t + 2 * c + j;
-          sx[t][j] = tok < p.T ? p.sx[int64_t(tok) * p.KB + kb] : 127u;
+          sx[u][t][j] = in && tok < p.T ? p.sx[int64_t(tok) * p.KB + kb] : 127u;
         }
       }
+#pragma unroll
+      for (int m = 0; m < NW; ++m) sw[u][m] = in ? p.sw[m][int64_t(row0 / 128) * p.KB + kb] : 127u;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int m = 0; m < NW; ++m) {
 #pragma unroll
@@ -94,10 +105,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 2) fp8_rows_kernel(const Call
           float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            mma_e4m3(d, word(w[m][0], 2 * s), word(w[m][1], 2 * s), word(w[m][0], 2 * s + 1), word(w[m][1], 2 * s + 1),
-                     word(x[t], 2 * s), word(x[t], 2 * s + 1));
+            mma_e4m3(d, word(w[u][m][0], 2 * s), word(w[u][m][1], 2 * s), word(w[u][m][0], 2 * s + 1),
+                     word(w[u][m][1], 2 * s + 1), word(x[u][t], 2 * s), word(x[u][t], 2 * s + 1));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][t][i] = add_scaled(acc[m][t][i], d[i], sx[t][i & 1], sw[m]);
+          for (int i = 0; i < 4; ++i) acc[m][t][i] = add_scaled(acc[m][t][i], d[i], sx[u][t][i & 1], sw[u][m]);
         }
       }
     }
@@ -150,21 +161,28 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 2) fp8_rows_kernel(const Call
   if (rank == 0 && r == 0) p.scales[int64_t(tok) * ((p.N + 127) / 128) + (blockIdx.x >> 3)] = uint8_t(b);
 }
 
-template <int NW, int NT, bool G>
+template <int NW, int NT, int U, bool G>
 cudaError_t launch(const Call& c, cudaStream_t s) {
   const unsigned ctas = unsigned((c.N + 15) / 16);
   const dim3 block(kRowsWarps * 32);
-  if (G) return launch_pdl_cluster(fp8_rows_kernel<NW, NT, G>, dim3((ctas + 7) / 8 * 8), block, dim3(8), 0, s, c);
-  return launch_pdl(fp8_rows_kernel<NW, NT, G>, dim3(ctas), block, 0, s, c);
+  if (G) return launch_pdl_cluster(fp8_rows_kernel<NW, NT, U, G>, dim3((ctas + 7) / 8 * 8), block, dim3(8), 0, s, c);
+  return launch_pdl(fp8_rows_kernel<NW, NT, U, G>, dim3(ctas), block, 0, s, c);
+}
+
+// G: results to 8 bits.  U: a warp of a long row keeps 8 KB of weights in flight, which the weights of
+// a short one do not fill and which two tiles of tokens leave no registers for.
+template <int NW, bool G>
+cudaError_t launch_tokens(const Call& c, cudaStream_t s) {
+  if (c.T > 8) return launch<NW, 2, 2 / NW, G>(c, s);
+  return c.KB > 2 * kRowsWarps ? launch<NW, 1, 4 / NW, G>(c, s) : launch<NW, 1, 2 / NW, G>(c, s);
 }
 
 }  // namespace
 
 namespace fp8 {
 cudaError_t launch_rows(const Call& c, cudaStream_t s) {
-  if (!c.w[1]) return c.T <= 8 ? launch<1, 1, false>(c, s) : launch<1, 2, false>(c, s);
-  if (!c.codes) return c.T <= 8 ? launch<2, 1, false>(c, s) : launch<2, 2, false>(c, s);
-  return c.T <= 8 ? launch<2, 1, true>(c, s) : launch<2, 2, true>(c, s);
+  if (!c.w[1]) return launch_tokens<1, false>(c, s);
+  return c.codes ? launch_tokens<2, true>(c, s) : launch_tokens<2, false>(c, s);
 }
 }  // namespace fp8
 }  // namespace scion
