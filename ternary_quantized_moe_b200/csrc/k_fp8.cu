@@ -795,22 +795,51 @@ cudaError_t max_clusters(int n, int* count) {
   return cudaOccupancyMaxActiveClusters(count, fp8_stream_kernel<1>, &cfg);
 }
 
+// Shape of a stream launch and what it is expected to take.
+struct StreamPlan {
+  int bn, t_tiles, n_tiles, splits;
+  double us;
+};
+
+// Tokens per tile: the accumulators (nw bn columns) and the scale words share 512 columns of tensor
+// memory, so 256 at most (208 for two matrices); narrower tiles give more CTAs, and tiles of up to
+// 128 / nw tokens can split K over a cluster.  The estimate is a fit to single launches: a wave costs
+// 2.4 us (5.5 with a cluster's exchange; more for tiles wider than 128 tokens) and, per block of K,
+// 0.2 + 0.0013 bn us (two matrices: 6.5 and 0.35 + 0.0035 bn), within 20% of what was measured from
+// 32 to 2048 tokens.
+StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
+  StreamPlan best{};
+  for (int most : {256, 128, 64}) {
+    StreamPlan p;
+    if (nw == 2) most = std::min(most, 208);
+    p.n_tiles = (N + 127) / 128, p.t_tiles = (T + most - 1) / most;
+    p.bn = ((T + p.t_tiles - 1) / p.t_tiles + 15) / 16 * 16;
+    const int64_t tiles = int64_t(p.n_tiles) * p.t_tiles;
+    // as many CTAs per tile as run at once (the sums of a wide tile would leave too little shared
+    // memory for the ring).  16 tiles of 64 tokens, K = 4096: 7.8 us with clusters of 6, 13.5 with
+    // clusters of 8, of which 15 fit.
+    p.splits = p.bn > 128 / nw ? 1 : std::min(8, KB);
+    while (p.splits > 1 && L->clusters[p.splits] < tiles) --p.splits;
+    const double waves = double((tiles * p.splits + L->sms - 1) / L->sms);
+    const double start = (p.splits > 1 ? (nw == 1 ? 5.5 : 6.5) : 2.4) + 0.032 * std::max(0, p.bn - 128);
+    p.us = waves * (start + (KB + p.splits - 1) / p.splits * (nw == 1 ? 0.2 + 0.0013 * p.bn : 0.35 + 0.0035 * p.bn));
+    if (!best.bn || p.us < best.us) best = p;
+  }
+  return best;
+}
+
+// The same for the pair kernel, fitted the same way.
+double pair_us(const scion_fp8* L, int nw, int T, int N, int KB) {
+  const int64_t tiles = int64_t((T + 255) / 256) * (nw == 1 ? (N + 255) / 256 : (N + 127) / 128);
+  const int pairs = std::max(1, L->sms / 2);
+  return (nw == 1 ? 4.5 : 5.4) + double((tiles + pairs - 1) / pairs) * (1.7 + 0.26 * KB);
+}
+
 template <int NW>
-int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, cudaStream_t s) {
+int launch_stream(const scion_fp8* L, const StreamPlan& plan, StreamParams& p, const uint8_t* x, int T, cudaStream_t s) {
   p.w[0] = L->w[0], p.w[1] = L->w[NW - 1];
-  const int n_tiles = (p.N + 127) / 128;
-  // tokens of a tile: the accumulators (NW bn columns) and the scale words share 512 columns of
-  // tensor memory; narrower tiles where the widest would leave SMs without one
-  int most = NW == 1 ? 256 : 208;
-  while (most > 64 && n_tiles * ((T + most - 1) / most) < L->sms / 2) most = most > 128 ? 128 : 64;
-  const int t_tiles = (T + most - 1) / most;
-  p.bn = ((T + t_tiles - 1) / t_tiles + 15) / 16 * 16;
-  const int ctas = n_tiles * t_tiles;
-  // as many CTAs per tile as run at once (the sums of a wide tile would leave too little shared memory
-  // for the ring).  16 tiles of 64 tokens, K = 4096: 7.8 us with clusters of 6, 13.5 with clusters of 8,
-  // of which 15 fit.
-  int splits = p.bn > 128 / NW ? 1 : std::min(8, p.KB);
-  while (splits > 1 && L->clusters[splits] < ctas) --splits;
+  p.bn = plan.bn;
+  const int splits = plan.splits;
   p.sfb_cols = p.bn > 128 ? 8 : 4;
   p.sf_col = NW * p.bn;
   p.tmem_cols = int(tmem_cols_pow2(p.sf_col + kSfSlots * (4 * NW + p.sfb_cols)));
@@ -821,14 +850,15 @@ int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, 
   const uint32_t stage = kStageBlocks<NW> * (NW * 16384 + p.bn * 128);
   const uint32_t fixed = 2048 + (splits > 1 ? (p.bn + splits - 1) / splits * splits * NW * 512 : 0);
   // two CTAs per SM where there are more than SMs
-  const uint32_t budget = ctas * splits > L->sms ? std::max<uint32_t>(share, 113 * 1024) : kSmem;
+  const bool crowded = int64_t(plan.n_tiles) * plan.t_tiles * splits > L->sms;
+  const uint32_t budget = crowded ? std::max<uint32_t>(share, 113 * 1024) : kSmem;
   const int range = (p.KB + splits - 1) / splits;  // K blocks of a CTA, at most
   p.stages = std::max(1, std::min({kMaxStages, int((budget - fixed) / stage), (range + kStageBlocks<NW> - 1) / kStageBlocks<NW>}));
   const uint32_t smem = std::max({fixed + p.stages * stage, uint32_t(2048 + NW * p.bn * 512), share});
   if (smem > kSmem) return SCION_EINVAL;
   int st = make_tmap_codes(&p.x, x, T, L->desc.k, p.bn);
   if (st != SCION_OK) return st;
-  return status(launch_pdl_cluster(fp8_stream_kernel<NW>, dim3(splits, n_tiles, t_tiles), dim3(kStreamThreads),
+  return status(launch_pdl_cluster(fp8_stream_kernel<NW>, dim3(splits, plan.n_tiles, plan.t_tiles), dim3(kStreamThreads),
                                    dim3(splits, 1, 1), smem, s, p));
 }
 
@@ -837,11 +867,6 @@ int launch_stream(const scion_fp8* L, StreamParams& p, const uint8_t* x, int T, 
 // tokens: 8 MB 4.0 against 6.1, 22 MB 11.0 against 8.5, 67 MB 22.8 against 15.3.
 bool use_rows(const Call& c) {
   return c.T <= 8 || (c.T <= 16 && int64_t(c.N) * c.K * (c.w[1] ? 2 : 1) <= (12 << 20));
-}
-
-// The pair kernel where its tiles fill the SMs and rows can be stored in 16-byte pieces.
-bool use_pair(const scion_fp8* L, int T, bool aligned) {
-  return aligned && T > 256;
 }
 
 template <int EPI>
@@ -944,11 +969,12 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
   p.base = base, p.out = out, p.out_bf16 = out_type == SCION_BF16;
   p.vec = p.N % 4 == 0 && !scion::misaligned(base, 16) && !scion::misaligned(out, 16);
   const bool rows16 = int64_t(p.N) * (p.out_bf16 ? 2 : 4) % 16 == 0 && p.vec;
-  if (scion::use_pair(L, T, rows16))
+  const scion::StreamPlan plan = scion::plan_stream(L, 1, T, p.N, p.KB);
+  if (rows16 && scion::pair_us(L, 1, T, p.N, p.KB) < plan.us)  // (it stores 16-byte pieces of rows)
     return base         ? scion::launch_pair<scion::kPairBase>(L, p, x_codes, T, s)
            : p.out_bf16 ? scion::launch_pair<scion::kPairBf16>(L, p, x_codes, T, s)
                         : scion::launch_pair<scion::kPairF32>(L, p, x_codes, T, s);
-  return scion::launch_stream<1>(L, p, x_codes, T, s);
+  return scion::launch_stream<1>(L, plan, p, x_codes, T, s);
 }
 
 extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* L,
@@ -965,10 +991,11 @@ extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_
   if (scion::use_rows(c)) return scion::status(scion::fp8::launch_rows(c, s));
   scion::StreamParams p = scion::params(L, x_scales, T);
   p.out = h_bf16, p.codes = h_codes, p.scales = h_scales;
-  if (scion::use_pair(L, T, true))
+  const scion::StreamPlan plan = scion::plan_stream(L, 2, T, p.N, p.KB);
+  if (scion::pair_us(L, 2, T, p.N, p.KB) < plan.us)
     return h_codes ? scion::launch_pair<scion::kPairGatedCodes>(L, p, x_codes, T, s)
                    : scion::launch_pair<scion::kPairGatedBf16>(L, p, x_codes, T, s);
-  return scion::launch_stream<2>(L, p, x_codes, T, s);
+  return scion::launch_stream<2>(L, plan, p, x_codes, T, s);
 }
 
 extern "C" int scion_fp8_check(const scion_fp8* L, void* stream) {
