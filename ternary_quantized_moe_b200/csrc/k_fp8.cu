@@ -110,21 +110,28 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// The results of `count` (at most B) tokens t, t + step, ...: features n .. n + 3 of this lane.
+// The base of `count` (at most B) tokens t, t + step, ...: columns n .. n + 3 of this lane.
+template <int B>
+__device__ __forceinline__ void load_tokens(const StreamParams& p, float4 (&b)[B], int t, int step, int count, int n) {
+#pragma unroll
+  for (int i = 0; i < B; ++i) {
+    b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < count && n < p.N) b[i] = *reinterpret_cast<const float4*>(p.base + int64_t(t + i * step) * p.N + n);
+  }
+}
+
+// The results of those tokens.  Features n .. n + 3 of this lane; where rows cannot be stored in such
+// pieces (p.vec = 0, a plain layer) lane, lane + 32, ... of the tile, which keeps a warp's stores
+// together.
 template <int NW, int B>
-__device__ __forceinline__ void store_tokens(const StreamParams& p, float4 (&v)[B][NW], int t, int step, int count, int n,
-                                             int lane) {
+__device__ __forceinline__ void store_tokens(const StreamParams& p, float4 (&v)[B][NW], const float4 (&b)[B], int t, int step,
+                                             int count, int n, int lane) {
   if (NW == 1) {
     if (p.vec) {  // N a multiple of 4, rows aligned: all four or none
       if (n >= p.N) return;
       if (p.base) {
-        float4 b[B];
 #pragma unroll
-        for (int i = 0; i < B; ++i)
-          if (i < count) b[i] = *reinterpret_cast<const float4*>(p.base + int64_t(t + i * step) * p.N + n);
-#pragma unroll
-        for (int i = 0; i < B; ++i)
-          if (i < count) v[i][0].x += b[i].x, v[i][0].y += b[i].y, v[i][0].z += b[i].z, v[i][0].w += b[i].w;
+        for (int i = 0; i < B; ++i) v[i][0].x += b[i].x, v[i][0].y += b[i].y, v[i][0].z += b[i].z, v[i][0].w += b[i].w;
       }
 #pragma unroll
       for (int i = 0; i < B; ++i) {
@@ -138,16 +145,18 @@ __device__ __forceinline__ void store_tokens(const StreamParams& p, float4 (&v)[
       }
       return;
     }
+    const int n0 = n - 3 * lane;
+#pragma unroll
     for (int i = 0; i < B; ++i) {
       if (i >= count) break;
-      const int64_t at = int64_t(t + i * step) * p.N + n;
+      const int64_t at = int64_t(t + i * step) * p.N + n0;
       const float o[4] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (n + j >= p.N) break;
-        const float s = p.base ? p.base[at + j] + o[j] : o[j];
-        if (p.out_bf16) static_cast<bf16*>(p.out)[at + j] = __float2bfloat16_rn(s);
-        else static_cast<float*>(p.out)[at + j] = s;
+        if (n0 + 32 * j >= p.N) break;
+        const float s = p.base ? p.base[at + 32 * j] + o[j] : o[j];
+        if (p.out_bf16) static_cast<bf16*>(p.out)[at + 32 * j] = __float2bfloat16_rn(s);
+        else static_cast<float*>(p.out)[at + 32 * j] = s;
       }
     }
     return;
@@ -375,13 +384,20 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
       __syncwarp();
       if (splits > 1 && lane < min(splits, nt)) mbar_arrive_remote(map_cluster_rank(sums_full, lane));
     }
+    constexpr int kBatch = 4;  // tokens per warp at a time: their loads and reductions overlap
+    const int n = row0 + 4 * lane, first = tok0 + rank;
+    const bool read_base = NW == 1 && p.base && p.vec;
+    float4 base[kBatch];
+    if (read_base) load_tokens(p, base, first + (warp - 2) * splits, 8 * splits, (mine - (warp - 2) + 7) / 8, n);
     // (an aborted CTA sends nothing: its owners' waits run out, and the status word says so)
     if (splits == 1) asm volatile("bar.sync 2, 256;" ::: "memory");
     else if (mine > 0) ok = named_bar_and(2, 256, mbar_wait_cluster(sums_full, 0, abort_flag, p.err));
     if (ok) {
-      const uint32_t src = (splits == 1 ? ring : sums) + 16 * lane;
-      constexpr int kBatch = 4;  // tokens per warp at a time: their loads and reductions overlap
+      const bool spread = NW == 1 && !p.vec;
+      const uint32_t src = (splits == 1 ? ring : sums) + (spread ? 4 : 16) * lane;
       for (int j0 = warp - 2; j0 < mine; j0 += 8 * kBatch) {
+        const int count = (mine - j0 + 7) / 8;
+        if (read_base && j0 != warp - 2) load_tokens(p, base, first + j0 * splits, 8 * splits, count, n);
         float4 v[kBatch][NW];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
@@ -390,15 +406,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
         for (int r = 0; r < splits; ++r) {
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
-            if (j0 + 8 * i >= mine) break;
+            if (i >= count) break;
 #pragma unroll
             for (int m = 0; m < NW; ++m) {
-              const float4 a = lds_f4(src + (((j0 + 8 * i) * splits + r) * NW + m) * 512);
+              const uint32_t at = src + (((j0 + 8 * i) * splits + r) * NW + m) * 512;
+              const float4 a = spread ? make_float4(lds_f32(at), lds_f32(at + 128), lds_f32(at + 256), lds_f32(at + 384)) : lds_f4(at);
               v[i][m].x += a.x, v[i][m].y += a.y, v[i][m].z += a.z, v[i][m].w += a.w;
             }
           }
         }
-        store_tokens<NW, kBatch>(p, v, tok0 + rank + j0 * splits, 8 * splits, (mine - j0 + 7) / 8, row0 + 4 * lane, lane);
+        store_tokens<NW, kBatch>(p, v, base, first + j0 * splits, 8 * splits, count, n, lane);
       }
     }
     tc_fence_before();
