@@ -10,6 +10,8 @@
 namespace scion {
 namespace fp8 {
 
+inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
 // One product call: out = base + W x (w[1] null), or h = silu(W0 x) (W1 x) to bf16 or codes and scales.
 struct Call {
   const uint8_t* x;

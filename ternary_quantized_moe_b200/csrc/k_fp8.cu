@@ -781,8 +781,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
 }
 
 // ------------------------------------------------------------------ host side
-inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
 // Tensor map of an e4m3 matrix [rows][K]: boxes of 128 columns x box_rows, 128-byte swizzle.
 int make_tmap_codes(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, int box_rows) {
   const auto fn = encode_tiled_fn();
@@ -927,9 +925,9 @@ extern "C" int scion_fp8_create(const scion_fp8_desc* D, void* stream, scion_fp8
   if (!out) return SCION_EINVAL;
   *out = nullptr;
   if (!D || D->n < 1 || D->n > (1 << 20) || D->k < 16 || D->k % 16 || D->k > 65536) return SCION_EINVAL;
-  if (!D->w_codes || !D->w_scales || scion::misaligned(D->w_codes, 16)) return SCION_EINVAL;
+  if (!D->w_codes || !D->w_scales || scion::fp8::misaligned(D->w_codes, 16)) return SCION_EINVAL;
   if (!D->up_codes != !D->up_scales) return SCION_EINVAL;
-  if (D->up_codes && (D->n % 16 || scion::misaligned(D->up_codes, 16))) return SCION_EINVAL;
+  if (D->up_codes && (D->n % 16 || scion::fp8::misaligned(D->up_codes, 16))) return SCION_EINVAL;
   scion_fp8* L = new (std::nothrow) scion_fp8;
   if (!L) return SCION_ENOMEM;
   L->desc = *D;
@@ -975,8 +973,8 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
                                  const float* base, void* out, int out_type, void* stream) {
   if (!L || L->desc.up_codes || T < 0 || (out_type != SCION_F32 && out_type != SCION_BF16)) return SCION_EINVAL;
   if (T == 0) return SCION_OK;
-  if (!x_codes || !x_scales || !out || scion::misaligned(x_codes, 16)) return SCION_EINVAL;
-  if (scion::misaligned(base, 4) || scion::misaligned(out, out_type == SCION_F32 ? 4 : 2)) return SCION_EINVAL;
+  if (!x_codes || !x_scales || !out || scion::fp8::misaligned(x_codes, 16)) return SCION_EINVAL;
+  if (scion::fp8::misaligned(base, 4) || scion::fp8::misaligned(out, out_type == SCION_F32 ? 4 : 2)) return SCION_EINVAL;
   if (out_type == SCION_BF16 && static_cast<const void*>(base) == out && base) return SCION_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);
@@ -984,7 +982,7 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
   if (scion::use_rows(c)) return scion::status(scion::fp8::launch_rows(c, s));
   scion::StreamParams p = scion::params(L, x_scales, T);
   p.base = base, p.out = out, p.out_bf16 = out_type == SCION_BF16;
-  p.vec = p.N % 4 == 0 && !scion::misaligned(base, 16) && !scion::misaligned(out, 16);
+  p.vec = p.N % 4 == 0 && !scion::fp8::misaligned(base, 16) && !scion::fp8::misaligned(out, 16);
   const bool rows16 = int64_t(p.N) * (p.out_bf16 ? 2 : 4) % 16 == 0 && p.vec;
   const scion::StreamPlan plan = scion::plan_stream(L, 1, T, p.N, p.KB);
   if (rows16 && scion::pair_us(L, 1, T, p.N, p.KB) < plan.us)  // (it stores 16-byte pieces of rows)
@@ -999,8 +997,8 @@ extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_
   if (!L || !L->desc.up_codes || T < 0) return SCION_EINVAL;
   if (T == 0) return SCION_OK;  // (empty tensors have null addresses)
   if (!h_codes != !h_scales || !h_codes == !h_bf16) return SCION_EINVAL;
-  if (!x_codes || !x_scales || scion::misaligned(x_codes, 16) || scion::misaligned(h_bf16, 16) ||
-      scion::misaligned(h_codes, 16))
+  if (!x_codes || !x_scales || scion::fp8::misaligned(x_codes, 16) || scion::fp8::misaligned(h_bf16, 16) ||
+      scion::fp8::misaligned(h_codes, 16))
     return SCION_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);

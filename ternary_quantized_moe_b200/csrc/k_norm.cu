@@ -4,7 +4,8 @@
 // All three are bound by HBM: one read of every input, one write of every output, nothing kept in
 // memory in between.  A thread holds 8 consecutive columns (16 bytes of bf16, 32 of fp32 per load
 // and lane), so a group of 128 columns is half a warp and its largest magnitude one redux over 16
-// lanes; the loads of a warp cover whole 32-byte sectors.
+// lanes; the loads of a warp cover whole 32-byte sectors.  Programmatic dependent launch lets a call's
+// blocks start as its predecessor's drain.
 #include <math.h>
 
 #include <algorithm>
@@ -52,6 +53,8 @@ struct NormParams {
 template <typename X, typename R, int CPT>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
   __shared__ float part[32];
+  pdl_trigger();
+  pdl_wait();
   const int64_t row = int64_t(blockIdx.x) * p.d;
   const int chunks = p.d >> 3, nt = blockDim.x;
   float v[CPT][8];
@@ -112,10 +115,9 @@ cudaError_t launch_norm(const NormParams& p, int T, cudaStream_t s) {
   const int chunks = p.d >> 3;
   const int cpt = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
   const int nt = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
-  if (cpt == 1) rmsnorm_kernel<X, R, 1><<<T, nt, 0, s>>>(p);
-  else if (cpt == 2) rmsnorm_kernel<X, R, 2><<<T, nt, 0, s>>>(p);
-  else rmsnorm_kernel<X, R, 4><<<T, nt, 0, s>>>(p);
-  return cudaGetLastError();
+  if (cpt == 1) return launch_pdl(rmsnorm_kernel<X, R, 1>, dim3(T), dim3(nt), 0, s, p);
+  if (cpt == 2) return launch_pdl(rmsnorm_kernel<X, R, 2>, dim3(T), dim3(nt), 0, s, p);
+  return launch_pdl(rmsnorm_kernel<X, R, 4>, dim3(T), dim3(nt), 0, s, p);
 }
 
 // ------------------------------------------------------------------ quantizers
@@ -124,6 +126,8 @@ template <typename S>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const S* __restrict__ src, int64_t rows, int cols,
                                                             int groups, uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
+  pdl_trigger();
+  pdl_wait();
   const int64_t n = rows * groups;
   const int64_t per = int64_t(gridDim.x) * 16;
   // the two half warps of a warp walk neighbouring groups; the bound is rounded up to whole warps
@@ -145,6 +149,8 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const S* __restric
                                                               int groups, uint8_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales) {
   __shared__ uint32_t part[8];
+  pdl_trigger();
+  pdl_wait();
   const int64_t rb = blockIdx.x / groups;
   const int g = int(blockIdx.x - rb * groups);
   const int c = g * 128 + 8 * (threadIdx.x & 15);
@@ -184,16 +190,12 @@ cudaError_t launch_quantize(const S* src, int64_t rows, int cols, int block_rows
   const int groups = (cols + 127) / 128;
   if (block_rows == 1) {
     const int64_t ctas = (rows * groups + 15) / 16;
-    quantize_rows_kernel<S><<<unsigned(std::min<int64_t>(ctas, 1 << 20)), 256, 0, s>>>(src, rows, cols, groups, codes,
-                                                                                      scales);
-  } else {
-    quantize_blocks_kernel<S><<<unsigned((rows + 127) / 128 * groups), 256, 0, s>>>(src, rows, cols, groups, codes,
-                                                                                   scales);
+    return launch_pdl(quantize_rows_kernel<S>, dim3(unsigned(std::min<int64_t>(ctas, 1 << 20))), dim3(256), 0, s, src, rows,
+                      cols, groups, codes, scales);
   }
-  return cudaGetLastError();
+  return launch_pdl(quantize_blocks_kernel<S>, dim3(unsigned((rows + 127) / 128 * groups)), dim3(256), 0, s, src, rows, cols,
+                    groups, codes, scales);
 }
-
-inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 }  // namespace
 }  // namespace scion
@@ -206,7 +208,7 @@ extern "C" int scion_fp8_quantize_device(int src_type, const void* src, int64_t 
   if (rows > (int64_t(1) << 40) || (block_rows == 128 && (rows + 127) / 128 * ((cols + 127) / 128) > 0x7fffffff))
     return SCION_EINVAL;
   if (rows == 0) return SCION_OK;
-  if (!src || !codes || !scales || scion::misaligned(src, 16) || scion::misaligned(codes, 16)) return SCION_EINVAL;
+  if (!src || !codes || !scales || scion::fp8::misaligned(src, 16) || scion::fp8::misaligned(codes, 16)) return SCION_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       src_type == SCION_F32
@@ -226,7 +228,7 @@ extern "C" int scion_rmsnorm_forward(const void* x, int x_type, const void* resi
   if (!x || !weight) return SCION_EINVAL;
   for (const void* p : {x, resid, weight, static_cast<const void*>(resid_out), static_cast<const void*>(y_bf16),
                         static_cast<const void*>(y_codes)})
-    if (scion::misaligned(p, 16)) return SCION_EINVAL;
+    if (scion::fp8::misaligned(p, 16)) return SCION_EINVAL;
   // in place on x only where an element is as wide (a thread then overwrites what it alone has read)
   if (resid_out == x && resid_type != x_type) return SCION_EINVAL;
   scion::NormParams p{x,       resid,    static_cast<const __nv_bfloat16*>(weight), resid_out, static_cast<__nv_bfloat16*>(y_bf16),
