@@ -105,9 +105,10 @@ struct RingPos {
   }
 };
 
-// A float into the shared memory of another CTA of the cluster (or this one).
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Four floats into the shared memory of another CTA of the cluster (or this one).
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 
 // The base of `count` (at most B) tokens t, t + step, ...: columns n .. n + 3 of this lane.
@@ -232,8 +233,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
   const uint32_t tmem = bars.tmem_slot;
   volatile int* abort_flag = &bars.abort_flag;
   pdl_trigger();
-  pdl_wait();
 
+  // (every role that touches global memory waits for the predecessor grid itself, as late as it can)
   bool joined = splits == 1;
   // the loops over K of warps 0 and 1 are run by the whole warp, with one lane (elect_one) issuing
   if (warp == 0) {
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
     int i = 0;
     uint32_t st = ring;
     bool ok = true;
+    pdl_wait();
     for (int kb = kb0; kb < kb1; kb += kStageBlocks<NW>, ++i) {
       if (i >= p.stages) ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * at.slot, at.parity ^ 1, abort_flag, p.err));
       if (!ok) break;
@@ -310,6 +312,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
     const int group = (warp - 2) >> 2;
     bool ok = true;
+    pdl_wait();
     if (group == 0) {
       // scale words: each of the four warps writes them to its own lane quarter
       const int q0 = kb0 / 4, q1 = (kb1 - 1) / 4;
@@ -371,13 +374,20 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
 #pragma unroll
             for (int i = 0; i < 16; ++i) sts_f32(dst + i * (NW * 512), v[i]);
           } else {
-            int owner = c % splits, slot = c / splits;
+            // the warp's 32 features of 16 tokens, turned through its own part of the (free) ring so
+            // that a lane sends four features at once: 8 lanes per token
+            const uint32_t turn = ring + (warp - 2) * 2304;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (c + i >= nt) break;
-              st_cluster_f32(map_cluster_rank(sums, owner) + ((slot * splits + rank) * NW + m) * 512 + feature, v[i]);
-              if (++owner == splits) owner = 0, ++slot;
+            for (int i = 0; i < 16; ++i) sts_f32(turn + i * 144 + lane * 4, v[i]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = 4 * i + (lane >> 3), owner = (c + t) % splits, slot = (c + t) / splits;
+              const float4 o = lds_f4(turn + t * 144 + (lane & 7) * 16);
+              if (c + t < nt)
+                st_cluster_f4(map_cluster_rank(sums, owner) + ((slot * splits + rank) * NW + m) * 512 + (warp & 3) * 128 + (lane & 7) * 16, o);
             }
+            __syncwarp();
           }
         }
       }
