@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(map_cluster_rank(sf_full + 8 * slot, 0));
+          if (lane == 0) mbar_arrive_remote_relaxed(map_cluster_rank(sf_full + 8 * slot, 0));
           ++sq;
         }
         // the next round, or the first of the next tile
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       tmem_ld64x2(acc0, acc1, v);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(released);
+      if (lane == 0) mbar_arrive_remote_relaxed(released);
       const int64_t tok = int64_t(mt) * 256 + rank * 128 + row;
       const bool live = tok < p.T;
       if (!kGated) {
