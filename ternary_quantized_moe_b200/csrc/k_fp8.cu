@@ -34,8 +34,7 @@ typedef __nv_bfloat16 bf16;
 // the tokens the N side (bn of them, a multiple of 16), and the CTAs of a cluster split K, so that a
 // matrix of few tiles still spreads over the SMs.  Partial sums: the tokens of a tile are dealt to
 // the CTAs of the cluster; every CTA stores its sums of a token straight into the shared memory of
-// the token's owner (every warp then arrives on a barrier there), and the owner adds them in rank
-// order.  One barrier of the cluster, at the start, and none on the way out: an owner leaves when
+// the token's owner (counted by a barrier there), and the owner adds them in rank order.  One barrier of the cluster, at the start, and none on the way out: an owner leaves when
 // everything sent to it has arrived.
 // Roles: warp 0 TMA loads through a ring of stages, warp 1 the MMAs, warps 2..9 the
 // epilogue (two per lane quarter, alternate 16-token chunks), warps 2..5 also the scale words.  The
@@ -105,9 +104,11 @@ struct RingPos {
   }
 };
 
-// Four floats into the shared memory of another CTA of the cluster (or this one).
-__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+// Four floats into the shared memory of another CTA of the cluster (or this one), counted as 16 bytes
+// on a barrier there: the receiver needs no release from the sender, which would wait for its stores.
+__device__ __forceinline__ void st_async_f4(uint32_t addr, uint32_t bar, float4 v) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
                : "memory");
 }
 
@@ -220,9 +221,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
     if (NW == 2) tma_prefetch_map(&p.w[1]);
     for (int s = 0; s < p.stages; ++s) mbar_init(&bars.full[s], 1), mbar_init(&bars.empty[s], 1);
     for (int s = 0; s < kSfSlots; ++s) mbar_init(&bars.sf_full[s], 128), mbar_init(&bars.sf_empty[s], 1);
-    mbar_init(&bars.acc_full, 1), mbar_init(&bars.done, 1), mbar_init(&bars.sums, 8 * splits);
+    mbar_init(&bars.acc_full, 1), mbar_init(&bars.done, 1), mbar_init(&bars.sums, 1);
     bars.abort_flag = 0;
     fence_barrier_init();
+    mbar_arrive_expect_tx(&bars.sums, mine * splits * NW * 512);
   }
   if (warp == 1) tmem_alloc(&bars.tmem_slot, p.tmem_cols);
   tc_fence_before();
@@ -385,14 +387,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
               const int t = 4 * i + (lane >> 3), owner = (c + t) % splits, slot = (c + t) / splits;
               const float4 o = lds_f4(turn + t * 144 + (lane & 7) * 16);
               if (c + t < nt)
-                st_cluster_f4(map_cluster_rank(sums, owner) + ((slot * splits + rank) * NW + m) * 512 + (warp & 3) * 128 + (lane & 7) * 16, o);
+                st_async_f4(map_cluster_rank(sums, owner) + ((slot * splits + rank) * NW + m) * 512 + (warp & 3) * 128 + (lane & 7) * 16,
+                            map_cluster_rank(sums_full, owner), o);
             }
             __syncwarp();
           }
         }
       }
-      __syncwarp();
-      if (splits > 1 && lane < min(splits, nt)) mbar_arrive_remote(map_cluster_rank(sums_full, lane));
     }
     constexpr int kBatch = 4;  // tokens per warp at a time: their loads and reductions overlap
     const int n = row0 + 4 * lane, first = tok0 + rank;
@@ -625,13 +626,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       bool ok = true;
       const uint32_t low0 = umma_desc_low(ring);
       for (int tile = pair; tile < n_tiles && ok; tile += pairs, acc_parity ^= 1) {
-        if (tile != pair) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_empty, acc_parity, abort_flag, p.err));
         for (int kb = 0; kb < p.KB && ok; ++kb) {
           if ((kb & 3) == 0) {
             ok = mbar_wait_cluster(sf_full + 8 * sf.slot, sf.parity, abort_flag, p.err);
             tc_fence_after();
           }
           ok = __all_sync(0xffffffffu, ok && mbar_wait(full + 8 * at.slot, at.parity, abort_flag, p.err));
+          if (kb == 0 && tile != pair) {  // the operands are there; last, the accumulators
+            ok = __all_sync(0xffffffffu, ok && mbar_wait_cluster(acc_empty, acc_parity, abort_flag, p.err));
+            tc_fence_after();
+          }
           if (!ok) break;
           const uint32_t low = low0 + at.slot * (kPairStage >> 4);
           const uint32_t sfa = tmem + kPairSfCol + sf.slot * 12;

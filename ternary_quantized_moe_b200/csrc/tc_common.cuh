@@ -105,12 +105,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // Barriers that threads of another CTA of the cluster arrive on: the remote arrival (address from
-// mapa), and the bounded wait with acquire at cluster scope.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// The same without a release: for hand-overs of tensor memory, which tcgen05.wait and the tcgen05
-// fences order (a release at cluster scope waits over a thousand cycles for the thread's own stores).
+// mapa), and the bounded wait with acquire at cluster scope.  The arrival is without a release: it
+// hands over tensor memory, which tcgen05.wait and the tcgen05 fences order (a release at cluster
+// scope would wait over a thousand cycles for the thread's own stores).
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
