@@ -396,7 +396,7 @@ size_t scion_fp8_device_bytes(const scion_fp8* layer);
  * [T][ceil(k/128)]), out device [T][n] of out_type (SCION_F32 or SCION_BF16), base device fp32
  * [T][n] or NULL; with out_type SCION_F32 it may be out itself.  Products and sums in fp32, one
  * rounding to out_type.  A row's result is bit-reproducible for the same T and does not depend on
- * the other rows.  T >= 0 (T = 0 is a no-op).  x_codes 16-byte aligned, out and base aligned to
+ * the other rows.  0 <= T <= 2^21 (T = 0 is a no-op).  x_codes 16-byte aligned, out and base aligned to
  * their elements.  The handle holds no workspace: calls on one handle may overlap.  EINVAL (also
  * for a gated layer), ECUDA. */
 int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* layer, const float* base,
@@ -416,7 +416,8 @@ int scion_fp8_check(const scion_fp8* layer, void* stream);
 /* ------------------------------------------------------------ measurement
  * Kernel-level timing for benchmarks.  Between scion_profile_begin and
  * scion_profile_end, every kernel a forward launches is bracketed by a pair of CUDA
- * events recorded on the stream it is launched on, tagged with its stage:           */
+ * events recorded on the stream it is launched on, tagged with its stage (the block's kernels;
+ * the 8-bit dense operators are not recorded):                                      */
 enum {
   SCION_STAGE_ROUTER_F32 = 0,  /* fp32 router logits (FFMA) */
   SCION_STAGE_XPROJ = 1,       /* bf16 router + delta, shared gate/up + SwiGLU, correction A */

@@ -49,6 +49,7 @@ constexpr int kStageBlocks = 2 / NW;
 constexpr int kSfSlots = 4;  // ring of scale words, each slot for 4 K blocks (one byte each)
 constexpr uint32_t kNoScale = 0x7f7f7f7fu;  // words of rows past the end: 2^0
 constexpr uint32_t kSmem = 227 * 1024;
+constexpr int kMaxTokens = 1 << 21;  // token tiles stay within a grid's z, tiles within 32 bits
 
 struct StreamParams {
   CUtensorMap w[2], x;
@@ -985,12 +986,13 @@ extern "C" size_t scion_fp8_device_bytes(const scion_fp8* L) { return L ? L->dev
 
 extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* L,
                                  const float* base, void* out, int out_type, void* stream) {
-  if (!L || L->desc.up_codes || T < 0 || (out_type != SCION_F32 && out_type != SCION_BF16)) return SCION_EINVAL;
+  if (!L || L->desc.up_codes || T < 0 || T > scion::kMaxTokens || (out_type != SCION_F32 && out_type != SCION_BF16)) return SCION_EINVAL;
   if (T == 0) return SCION_OK;
   if (!x_codes || !x_scales || !out || scion::fp8::misaligned(x_codes, 16)) return SCION_EINVAL;
   if (scion::fp8::misaligned(base, 4) || scion::fp8::misaligned(out, out_type == SCION_F32 ? 4 : 2)) return SCION_EINVAL;
   if (out_type == SCION_BF16 && static_cast<const void*>(base) == out && base) return SCION_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  scion::count_launch();
   scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);
   c.base = base, c.out = out, c.out_bf16 = out_type == SCION_BF16;
   if (scion::use_rows(c)) return scion::status(scion::fp8::launch_rows(c, s));
@@ -1008,13 +1010,14 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
 
 extern "C" int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* L,
                                        void* h_bf16, uint8_t* h_codes, uint8_t* h_scales, void* stream) {
-  if (!L || !L->desc.up_codes || T < 0) return SCION_EINVAL;
+  if (!L || !L->desc.up_codes || T < 0 || T > scion::kMaxTokens) return SCION_EINVAL;
   if (T == 0) return SCION_OK;  // (empty tensors have null addresses)
   if (!h_codes != !h_scales || !h_codes == !h_bf16) return SCION_EINVAL;
   if (!x_codes || !x_scales || scion::fp8::misaligned(x_codes, 16) || scion::fp8::misaligned(h_bf16, 16) ||
       scion::fp8::misaligned(h_codes, 16))
     return SCION_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  scion::count_launch();
   scion::fp8::Call c = scion::call(L, x_codes, x_scales, T);
   c.out = h_bf16, c.codes = h_codes, c.scales = h_scales;
   if (scion::use_rows(c)) return scion::status(scion::fp8::launch_rows(c, s));

@@ -234,6 +234,7 @@ extern "C" int scion_rmsnorm_forward(const void* x, int x_type, const void* resi
   scion::NormParams p{x,       resid,    static_cast<const __nv_bfloat16*>(weight), resid_out, static_cast<__nv_bfloat16*>(y_bf16),
                       y_codes, y_scales, eps, d, (d + 127) / 128};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  scion::count_launch();
   using scion::launch_norm;
   const cudaError_t e = x_type == SCION_F32
                             ? (resid_type == SCION_F32 ? launch_norm<float, float>(p, T, s)

@@ -732,6 +732,8 @@ extern "C" int scion_profile_end(int n_stages, double* ms_total, int64_t* launch
   return cuda_status(err);
 }
 
+void scion::count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+
 extern "C" int64_t scion_kernel_launches(void) { return g_launches.load(); }
 
 extern "C" int scion_layer_set_option(scion_layer* L, int option, int value) {

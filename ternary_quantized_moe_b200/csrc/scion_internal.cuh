@@ -182,6 +182,8 @@ struct scion_layer {
 
 namespace scion {
 
+void count_launch();  // one more kernel of a forward entry point (scion_kernel_launches)
+
 // ---------------------------------------------------------------- launchers
 // k_format.cu
 cudaError_t launch_pack(int fmt, const int8_t* codes, const uint16_t* scales, int64_t n_groups, uint8_t* out,

@@ -259,6 +259,27 @@ def test_linear_scale_range(T):
     assert torch.isnan(out3[3:, 128:]).all() and torch.equal(out3[3:, :128], out[3:, :128])
 
 
+@pytest.mark.parametrize("T,K,N", [(3, 272, 132), (20, 2048, 264), (70, 528, 512), (300, 2048, 512), (300, 48, 260)])
+def test_linear_unaligned(T, K, N):
+    """Outputs, bases and scales that start at addresses aligned to one element only."""
+    c = Case(T, K, N)
+    sx = torch.empty(c.dsx.numel() + 1, dtype=torch.uint8, device=DEV)
+    sx[1:] = c.dsx.view(torch.uint8).flatten()
+    sw = torch.empty(c.w[0][1].size + 1, dtype=torch.uint8, device=DEV)
+    sw[1:] = dev_scales(c.w[0][1]).view(torch.uint8).flatten()
+    c.layer = tq.scion_fp8_create(dev_codes(c.w[0][0]), sw[1:])
+    base = torch.empty(T * N + 1, dtype=F32, device=DEV)
+    base[1:] = torch.from_numpy(c.base).to(DEV).flatten()
+    for out_type in (F32, BF16):
+        buf = torch.full((T * N + 2,), 7.0, dtype=out_type, device=DEV)
+        out = buf[1:-1].view(T, N)
+        tq.scion_fp8_forward(c.dx, sx[1:], T, c.layer, out)
+        c.check(out)
+        tq.scion_fp8_forward(c.dx, sx[1:], T, c.layer, out, base=base[1:].view(T, N))
+        c.check(out, c.base)
+        assert buf[0] == 7 and buf[-1] == 7
+
+
 GATED = [(1, 16, 16), (1, 2048, 512), (2, 128, 128), (7, 144, 112), (16, 512, 144), (33, 2048, 272), (50, 2048, 528),
          (64, 4112, 384), (65, 256, 1008), (100, 2064, 256), (129, 1024, 240), (257, 512, 528), (300, 2048, 512),
          (1025, 1024, 768), (600, 16, 16), (2600, 640, 1040)]
@@ -308,6 +329,68 @@ def test_gated_special_rows(T):
     c.x[1] = 0
     ref, err = gated_reference(c)
     R.check_codes(bytes_of(codes)[keep], bytes_of(scales)[keep], ref[keep], err[keep])
+
+
+# ------------------------------------------------------------------ far offsets
+@pytest.mark.parametrize("N", [4096, 4097])
+def test_linear_rows_past_32_bits(N):
+    """An output of more than 2^31 elements: its first and last rows."""
+    T, K = 540000, 16
+    c = Case(256, K, N)
+    x, sx = (t.view(torch.uint8).repeat(-(-T // 256), 1)[:T].contiguous() for t in (c.dx, c.dsx))
+    out = torch.empty((T, N), dtype=BF16, device=DEV)
+    tq.scion_fp8_forward(x, sx, T, c.layer, out)
+    last = (T - 1) // 256 * 256  # a whole copy of the rows, and the part of one at the end
+    c.check(out[:256])
+    assert torch.equal(out[last - 256:last], out[:256]) and torch.equal(out[last:], out[:T - last])
+
+
+def test_gated_rows_past_32_bits():
+    T, K, F = 540000, 16, 4112
+    c = Case(256, K, F, gated=True)
+    x, sx = (t.view(torch.uint8).repeat(-(-T // 256), 1)[:T].contiguous() for t in (c.dx, c.dsx))
+    codes, scales = torch.empty((T, F), dtype=torch.uint8, device=DEV), torch.empty((T, 33), dtype=torch.uint8, device=DEV)
+    tq.scion_fp8_gated_forward(x, sx, T, c.layer, h_codes=codes, h_scales=scales)
+    ref, err = gated_reference(c)
+    R.check_codes(bytes_of(codes[:256]), bytes_of(scales[:256]), ref, err)
+    last = (T - 1) // 256 * 256
+    for t in (codes, scales):
+        assert torch.equal(t[last - 256:last], t[:256]) and torch.equal(t[last:], t[:T - last])
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_weights_past_32_bits(T):
+    N, K = 1 << 20, 2064
+    c = Case(T, K, 128)
+    w = c.w[0][0]
+    wd, sd = dev_codes(w).view(torch.uint8).repeat(N // 128, 1), dev_scales(c.w[0][1]).view(torch.uint8).repeat(N // 128, 1)
+    want = c.run(F32)
+    c.layer = tq.scion_fp8_create(wd, sd)
+    out = torch.empty((T, N), dtype=F32, device=DEV)
+    tq.scion_fp8_forward(c.dx, c.dsx, T, c.layer, out)
+    c.check(out[:, :128].contiguous())
+    c.check(out[:, -128:].contiguous())
+    assert torch.equal(out[:, -128:], out[:, :128]) and want.shape == (T, 128)
+
+
+def test_norm_and_quantize_past_32_bits():
+    T, d = 270000, 8192
+    x, _, w = norm_case(64, d, BF16, None)
+    big = x.to(DEV).repeat(-(-T // 64), 1)[:T].contiguous()
+    y = torch.empty_like(big)
+    codes, scales = torch.empty((T, d), dtype=torch.uint8, device=DEV), torch.empty((T, 64), dtype=torch.uint8, device=DEV)
+    tq.scion_rmsnorm_forward(big, T, w.to(DEV), 1e-6, y=y, y_codes=codes, y_scales=scales)
+    last = (T - 1) // 64 * 64
+    check_norm(x, None, w, 1e-6, None, y[:64], codes[:64], scales[:64])
+    for t in (y, codes, scales):
+        assert torch.equal(t[last - 64:last], t[:64]) and torch.equal(t[last:], t[:T - last])
+    for block_rows in (1, 128):
+        q, s = tq.scion_fp8_quantize_device(big, block_rows=block_rows)
+        tail = T % 128  # (with block_rows 128 the last, shorter block of rows)
+        rq, rs = R.quantize(host(big[T - tail:]), block_rows)
+        np.testing.assert_array_equal(bytes_of(q[T - tail:]), rq)
+        np.testing.assert_array_equal(bytes_of(s[-rs.shape[0]:]), rs)
+        del q, s
 
 
 # ------------------------------------------------------------------ use
@@ -382,11 +465,22 @@ def test_python_refusals():
               lambda: tq.scion_fp8_gated_forward(g.dx, g.dsx, 4, g.layer),
               lambda: tq.scion_fp8_gated_forward(g.dx, g.dsx, 4, g.layer, h_codes=hc),
               lambda: tq.scion_fp8_gated_forward(g.dx, g.dsx, 4, g.layer, h=out.bfloat16(), h_codes=hc, h_scales=hs),
-              lambda: tq.scion_fp8_quantize_device(out[:, :24].contiguous())]
+              lambda: tq.scion_fp8_quantize_device(out[:, :24].contiguous()),
+              lambda: tq._check(tq._load().scion_fp8_forward(c.dx.data_ptr(), c.dsx.data_ptr(), (1 << 21) + 1, c.layer.handle,
+                                                             None, out.data_ptr(), 0, None), "scion_fp8_forward")]
     for f in einval:
         with pytest.raises(tq.ScionError) as e:
             f()
         assert e.value.status == tq.SCION_EINVAL
+
+
+def test_launches_are_counted():
+    c = Case(3, 256, 128)
+    before = tq.scion_kernel_launches()
+    c.run(F32)
+    tq.scion_rmsnorm_forward(torch.ones((2, 256), device=DEV), 2, torch.ones(256, dtype=BF16, device=DEV), 1e-6,
+                             y=torch.empty((2, 256), dtype=BF16, device=DEV))
+    assert tq.scion_kernel_launches() == before + 2
 
 
 def test_empty_batches():
