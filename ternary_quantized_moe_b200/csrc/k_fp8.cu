@@ -34,12 +34,13 @@ typedef __nv_bfloat16 bf16;
 // the tokens the N side (bn of them, a multiple of 16), and the CTAs of a cluster split K, so that a
 // matrix of few tiles still spreads over the SMs.  Partial sums: the tokens of a tile are dealt to
 // the CTAs of the cluster; every CTA stores its sums of a token straight into the shared memory of
-// the token's owner (counted by a barrier there), and the owner adds them in rank order.  One barrier of the cluster, at the start, and none on the way out: an owner leaves when
-// everything sent to it has arrived.
-// Roles: warp 0 TMA loads through a ring of stages, warp 1 the MMAs, warps 2..9 the
-// epilogue (two per lane quarter, alternate 16-token chunks), warps 2..5 also the scale words.  The
-// sums pass through shared memory, so that a warp finishes one token at a time with four features
-// per lane: one reduction for a token's scale, 128 features in whole sectors.
+// the token's owner (counted by a barrier there), and the owner adds them in rank order.  One barrier
+// of the cluster, at the start, and none on the way out: an owner leaves when everything sent to it
+// has arrived.
+// Roles: warp 0 TMA loads through a ring of stages, warp 1 the MMAs, warps 2..9 the epilogue (two per
+// lane quarter, alternate 16-token chunks), warps 2..5 also the scale words.  The sums pass through
+// shared memory, so that a warp finishes one token at a time with four features per lane: one
+// reduction for a token's scale, 128 features in whole sectors.
 constexpr int kStreamThreads = 320;
 constexpr int kMaxStages = 8;
 // K blocks of 128 per stage: waiting for a stage takes as long as four narrow MMAs, so a stage holds
@@ -71,25 +72,40 @@ struct Bars {
   int abort_flag;
 };
 
+// Scale bytes of an array [rows][KB]: its first byte and its end.
+struct Scales {
+  const uint8_t* first;
+  const uint8_t* end;
+};
+
+// The aligned word at `a`: what of it lies in the array.
+__device__ __forceinline__ uint32_t word_inside(const uint8_t* a, const Scales& s) {
+  if (a >= s.first && a + 4 <= s.end) return *reinterpret_cast<const uint32_t*>(a);
+  uint32_t w = 0;
+  for (int j = 0; j < 4; ++j)
+    if (a + j >= s.first && a + j < s.end) w |= uint32_t(a[j]) << (8 * j);
+  return w;
+}
+
 // Scale bytes of one row are read 16 K blocks at a time (a "round": four words of four blocks), so
-// that the loads of a round overlap and the next round's are in flight while the MMAs use this one;
-// blocks past the end read as 2^0.  `align`: 16-, 4- or 1-byte loads (alignment of the row starts).
-__device__ __forceinline__ uint4 scale_round(const uint8_t* row, int r, int KB, int align) {
-  if (align == 16) return *reinterpret_cast<const uint4*>(row + 16 * r);
-  uint32_t w[4];
+// that the loads of a round overlap and the next round's are in flight while the MMAs use this one.
+// `align`: alignment of the row starts (16, 4 or 1).  Bytes of blocks past the row's end are whatever
+// follows in the array; no MMA selects them.
+__device__ __forceinline__ uint4 scale_round(const Scales& s, int64_t row, int r, int KB, int align) {
+  const uint8_t* p = s.first + row * KB + 16 * r;
+  if (align == 16) return *reinterpret_cast<const uint4*>(p);
+  uint32_t w[5];
+  if (align == 4) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int kb = 16 * r + 4 * i;
-    w[i] = 0x7f7f7f7fu;
-    if (align == 4) {
-      if (kb < KB) w[i] = *reinterpret_cast<const uint32_t*>(row + kb);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (kb + j < KB) w[i] = (w[i] & ~(0xffu << (8 * j))) | (uint32_t(row[kb + j]) << (8 * j));
-    }
+    for (int i = 0; i < 4; ++i) w[i] = 16 * r + 4 * i < KB ? *reinterpret_cast<const uint32_t*>(p + 4 * i) : kNoScale;
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  // five aligned words around the sixteen bytes, shifted into place
+  const int off = int(reinterpret_cast<uintptr_t>(p) & 3);
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = word_inside(p - off + 4 * i, s);
+  return make_uint4(__funnelshift_r(w[0], w[1], 8 * off), __funnelshift_r(w[1], w[2], 8 * off),
+                    __funnelshift_r(w[2], w[3], 8 * off), __funnelshift_r(w[3], w[4], 8 * off));
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
@@ -320,15 +336,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
       // scale words: each of the four warps writes them to its own lane quarter
       const int q0 = kb0 / 4, q1 = (kb1 - 1) / 4;
       const int cols = (p.bn + 31) / 32;
+      const Scales sx{p.sx, p.sx + int64_t(p.T) * p.KB};
+      Scales sw[NW];
+#pragma unroll
+      for (int m = 0; m < NW; ++m) sw[m] = Scales{p.sw[m], p.sw[m] + int64_t((p.N + 127) / 128) * p.KB};
       uint4 wa[NW], wb[8];
       auto load = [&](int r) {
 #pragma unroll
-        for (int m = 0; m < NW; ++m) wa[m] = scale_round(p.sw[m] + int64_t(blockIdx.y) * p.KB, r, p.KB, p.sf_align);
+        for (int m = 0; m < NW; ++m) wa[m] = scale_round(sw[m], blockIdx.y, r, p.KB, p.sf_align);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const int t = tok0 + 32 * c + lane;
           wb[c] = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
-          if (c < cols && t < p.T) wb[c] = scale_round(p.sx + int64_t(t) * p.KB, r, p.KB, p.sf_align);
+          if (c < cols && t < p.T) wb[c] = scale_round(sx, t, r, p.KB, p.sf_align);
         }
       };
       load(q0 / 4);
@@ -667,6 +687,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     // scale words of this CTA's tokens (4 columns) and of all 256 weight rows (8 columns)
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
     const int blocks = (p.N + 127) / 128;
+    const Scales sx{p.sx, p.sx + int64_t(p.T) * p.KB};
+    const Scales sw0{p.sw[0], p.sw[0] + int64_t(blocks) * p.KB};
+    const uint8_t* second = p.sw[kGated ? 1 : 0];
+    const Scales sw1{second, second + int64_t(blocks) * p.KB};
     uint4 a[4], u, v;
     auto load = [&](int tile, int r) {
       int mt, nt;
@@ -676,11 +700,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         a[c] = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
-        if (tok0 + 32 * c < p.T) a[c] = scale_round(p.sx + int64_t(tok0 + 32 * c) * p.KB, r, p.KB, p.sf_align);
+        if (tok0 + 32 * c < p.T) a[c] = scale_round(sx, tok0 + 32 * c, r, p.KB, p.sf_align);
       }
-      u = scale_round(p.sw[0] + int64_t(b0) * p.KB, r, p.KB, p.sf_align);
+      u = scale_round(sw0, b0, r, p.KB, p.sf_align);
       v = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
-      if (b1 < blocks) v = scale_round(p.sw[kGated ? 1 : 0] + int64_t(b1) * p.KB, r, p.KB, p.sf_align);
+      if (b1 < blocks) v = scale_round(sw1, b1, r, p.KB, p.sf_align);
     };
     int sq = 0;
     bool ok = true;
