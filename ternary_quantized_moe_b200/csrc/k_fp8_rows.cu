@@ -45,12 +45,74 @@ __device__ __forceinline__ uint32_t word(const Bytes32& b, int i) {
   return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
 }
 
-// acc + v 2^(a - 127) 2^(b - 127) for scale bytes a and b, as two factors of the same sign of exponent,
-// so that nothing between overflows or underflows where the result does not.
-__device__ __forceinline__ float add_scaled(float acc, float v, uint32_t a, uint32_t b) {
-  const int e = int(a + b) - 254, e1 = e >> 1, e2 = e - e1;
-  const float f1 = __uint_as_float(uint32_t(e1 + 127) << 23), f2 = __uint_as_float(uint32_t(e2 + 127) << 23);
-  return (a == 255u || b == 255u) ? NAN : fmaf(v * f1, f2, acc);
+// 2^(a - 127) 2^(b - 127) for scale bytes a and b, as two factors of the same sign of exponent, so that
+// nothing between overflows or underflows where the product with a value does not.  Nearly always one
+// factor does and the other is 1.
+__device__ __forceinline__ float2 scale_factors(uint32_t a, uint32_t b) {
+  const int e = int(a + b) - 254;
+  if (a != 255u && b != 255u && unsigned(e + 126) <= 253u) return make_float2(__uint_as_float(uint32_t(e + 127) << 23), 1.f);
+  if (a == 255u || b == 255u) return make_float2(NAN, 1.f);
+  const int e1 = e >> 1, e2 = e - e1;
+  return make_float2(__uint_as_float(uint32_t(e1 + 127) << 23), __uint_as_float(uint32_t(e2 + 127) << 23));
+}
+
+// Row pointers of a lane: its two weight rows, its token rows (operand rows and the columns of its
+// sums), clamped to what exists (a row past the end repeats the last one; its sums are not used).
+template <int NW, int NT>
+struct Lane {
+  const uint8_t* w[NW][2];
+  const uint8_t* x[NT];
+  const uint8_t* sw[NW];
+  const uint8_t* sx[NT][2];
+};
+
+// U blocks of K, kRowsWarps apart, from block kb on: loads first, then the products.  kTail: the last
+// of a row, where blocks and parts of blocks may be missing.
+template <int NW, int NT, int U, bool kTail>
+__device__ __forceinline__ void blocks(const Call& p, const Lane<NW, NT>& l, int kb, int c, float (&acc)[NW][NT][4]) {
+  Bytes32 w[U][NW][2], x[U][NT];
+  uint32_t sw[U][NW], sx[U][NT][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int k = (kb + u * kRowsWarps) * 128 + 32 * c, left = kTail ? p.K - k : 128;
+#pragma unroll
+    for (int m = 0; m < NW; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[u][m][h] = load32(l.w[m][h] + k, left);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int b = kb + u * kRowsWarps, k = b * 128 + 32 * c, left = kTail ? p.K - k : 128;
+    const bool in = !kTail || b < p.KB;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      x[u][t] = load32(l.x[t] + k, left);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) sx[u][t][j] = in ? l.sx[t][j][b] : 127u;
+    }
+#pragma unroll
+    for (int m = 0; m < NW; ++m) sw[u][m] = in ? l.sw[m][b] : 127u;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int m = 0; m < NW; ++m) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          mma_e4m3(d, word(w[u][m][0], 2 * s), word(w[u][m][1], 2 * s), word(w[u][m][0], 2 * s + 1),
+                   word(w[u][m][1], 2 * s + 1), word(x[u][t], 2 * s), word(x[u][t], 2 * s + 1));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 f = scale_factors(sx[u][t][j], sw[u][m]);
+          acc[m][t][j] = fmaf(d[j] * f.y, f.x, acc[m][t][j]);
+          acc[m][t][j + 2] = fmaf(d[j + 2] * f.y, f.x, acc[m][t][j + 2]);
+        }
+      }
+    }
+  }
 }
 
 // NW matrices, NT tiles of 8 tokens, U blocks of K per warp with their loads in flight together, G:
@@ -61,57 +123,26 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 2) fp8_rows_kernel(const Call
   __shared__ uint32_t amax[8][8 * NT];                // [CTA of the cluster][token]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int row0 = blockIdx.x * 16;
+  Lane<NW, NT> l;
+#pragma unroll
+  for (int m = 0; m < NW; ++m) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) l.w[m][h] = p.w[m] + int64_t(min(row0 + g + 8 * h, p.N - 1)) * p.K;
+    l.sw[m] = p.sw[m] + int64_t(min(row0, p.N - 1) / 128) * p.KB;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l.x[t] = p.x + int64_t(min(8 * t + g, p.T - 1)) * p.K;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) l.sx[t][j] = p.sx + int64_t(min(8 * t + 2 * c + j, p.T - 1)) * p.KB;
+  }
   pdl_trigger();
   pdl_wait();
   float acc[NW][NT][4] = {};
-  // (a cluster's last CTAs may have no rows)
-  for (int kb0 = warp; kb0 < p.KB && row0 < p.N; kb0 += kRowsWarps * U) {
-    Bytes32 w[U][NW][2], x[U][NT];
-    uint32_t sw[U][NW], sx[U][NT][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = kb0 + u * kRowsWarps, k = kb * 128 + 32 * c, left = p.K - k;  // (left < 1 past the end)
-#pragma unroll
-      for (int m = 0; m < NW; ++m) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = row0 + g + 8 * h;
-          w[u][m][h] = load32(p.w[m] + int64_t(r) * p.K + k, r < p.N ? left : 0);
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = kb0 + u * kRowsWarps, k = kb * 128 + 32 * c, left = p.K - k;
-      const bool in = kb < p.KB;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        x[u][t] = load32(p.x + int64_t(8 * t + g) * p.K + k, 8 * t + g < p.T ? left : 0);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int tok = 8 * t + 2 * c + j;
-          sx[u][t][j] = in && tok < p.T ? p.sx[int64_t(tok) * p.KB + kb] : 127u;
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < NW; ++m) sw[u][m] = in ? p.sw[m][int64_t(row0 / 128) * p.KB + kb] : 127u;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int m = 0; m < NW; ++m) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            mma_e4m3(d, word(w[u][m][0], 2 * s), word(w[u][m][1], 2 * s), word(w[u][m][0], 2 * s + 1),
-                     word(w[u][m][1], 2 * s + 1), word(x[u][t], 2 * s), word(x[u][t], 2 * s + 1));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][t][i] = add_scaled(acc[m][t][i], d[i], sx[u][t][i & 1], sw[u][m]);
-        }
-      }
-    }
+  if (row0 < p.N) {  // (a cluster's last CTAs may have no rows)
+    int kb = warp;
+    for (; (kb + (U - 1) * kRowsWarps + 1) * 128 <= p.K; kb += kRowsWarps * U) blocks<NW, NT, U, false>(p, l, kb, c, acc);
+    for (; kb < p.KB; kb += kRowsWarps) blocks<NW, NT, 1, true>(p, l, kb, c, acc);
   }
 #pragma unroll
   for (int m = 0; m < NW; ++m)

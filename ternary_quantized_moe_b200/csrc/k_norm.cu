@@ -121,25 +121,41 @@ cudaError_t launch_norm(const NormParams& p, int T, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------ quantizers
-// Activations: a half warp per group of 128 columns of a row.
+// Activations: a half warp per group of 128 columns of a row, `per` rows per CTA (so that a group's row
+// is a 32-bit division: with a 64-bit one per group the kernel was bound by its instructions, 16384 x
+// 4096 bf16 in 52 us), four groups' loads in flight.
 template <typename S>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const S* __restrict__ src, int64_t rows, int cols,
-                                                            int groups, uint8_t* __restrict__ codes,
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const S* __restrict__ src, int64_t rows, int cols, int groups,
+                                                            int per, uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
+  constexpr int U = 4;
   pdl_trigger();
   pdl_wait();
-  const int64_t n = rows * groups;
-  const int64_t per = int64_t(gridDim.x) * 16;
-  // the two half warps of a warp walk neighbouring groups; the bound is rounded up to whole warps
-  for (int64_t g = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4); g < (n + 1) / 2 * 2; g += per) {
-    const int64_t row = g / groups;
-    const int c0 = int(g - row * groups) * 128 + 8 * (threadIdx.x & 15);
-    const bool in = g < n && c0 < cols;
-    float v[8] = {};
-    if (in) load8(src + row * cols + c0, v);
-    const uint32_t b = scale_byte(half_warp_max(mag8(v)));
-    if (in) *reinterpret_cast<uint2*>(codes + row * cols + c0) = code8(v, scale_inverse(b));
-    if (g < n && (threadIdx.x & 15) == 0) scales[g] = uint8_t(b);
+  const int64_t row0 = int64_t(blockIdx.x) * per;
+  const uint32_t n = uint32_t(min(int64_t(per), rows - row0)) * groups;
+  src += row0 * cols, codes += row0 * cols, scales += row0 * groups;
+  const int lane = threadIdx.x & 15;
+  // the bound is rounded up to whole warps (a warp's two half warps walk neighbouring groups)
+  for (uint32_t i0 = threadIdx.x >> 4; i0 < (n + 1) / 2 * 2; i0 += 16 * U) {
+    float v[U][8];
+    int64_t at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i0 + 16 * u, row = i / uint32_t(groups);
+      const int c = int(i - row * groups) * 128 + 8 * lane;
+      at[u] = i < n && c < cols ? int64_t(row) * cols + c : -1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
+      if (at[u] >= 0) load8(src + at[u], v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i0 + 16 * u;
+      if (i >= (n + 1) / 2 * 2) break;
+      const uint32_t b = scale_byte(half_warp_max(mag8(v[u])));
+      if (at[u] >= 0) *reinterpret_cast<uint2*>(codes + at[u]) = code8(v[u], scale_inverse(b));
+      if (i < n && lane == 0) scales[i] = uint8_t(b);
+    }
   }
 }
 
@@ -189,9 +205,11 @@ cudaError_t launch_quantize(const S* src, int64_t rows, int cols, int block_rows
                             cudaStream_t s) {
   const int groups = (cols + 127) / 128;
   if (block_rows == 1) {
-    const int64_t ctas = (rows * groups + 15) / 16;
-    return launch_pdl(quantize_rows_kernel<S>, dim3(unsigned(std::min<int64_t>(ctas, 1 << 20))), dim3(256), 0, s, src, rows,
-                      cols, groups, codes, scales);
+    // 64 groups per CTA where that leaves two CTAs for every SM; the grid stays within 2^31 - 1
+    int64_t per = std::max<int64_t>(1, std::min<int64_t>(64 / groups, rows / 296));
+    per = std::max(per, rows >> 30);
+    return launch_pdl(quantize_rows_kernel<S>, dim3(unsigned((rows + per - 1) / per)), dim3(256), 0, s, src, rows, cols,
+                      groups, int(per), codes, scales);
   }
   return launch_pdl(quantize_blocks_kernel<S>, dim3(unsigned((rows + 127) / 128 * groups)), dim3(256), 0, s, src, rows, cols,
                     groups, codes, scales);
