@@ -48,72 +48,99 @@ struct NormParams {
   int d, groups;
 };
 
-// One CTA per row; thread t holds the 8-column chunks t, t + blockDim, ...: the row stays in
-// registers between the statistic and the output.
+// The row of `lanes` threads (a warp, or the whole CTA with kBlock): thread t of them holds the 8-column
+// chunks t, t + lanes, ..., so that the row stays in registers between the statistic and the output.
+// y = (r w) rms: the products r w and their largest magnitude per group do not wait for the statistic,
+// and (rounding is monotonic, a scale a power of two) max |y| = max |r w| rms and y / s = (r w)(rms / s)
+// to the last bit.
+template <typename X, typename R, int CPT, bool kBlock>
+__device__ __forceinline__ void norm_row(const NormParams& p, int64_t r, int t, int lanes, float* part) {
+  const int64_t row = r * p.d;
+  const int chunks = p.d >> 3;
+  float v[CPT][8];
+  uint32_t m[CPT];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = t + i * lanes;
+    const bool in = c < chunks;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    if (in) {
+      w = __ldg(reinterpret_cast<const uint4*>(p.w + 8 * c));
+      load8(static_cast<const X*>(p.x) + row + 8 * c, v[i]);
+      if (p.resid) {
+        float o[8];
+        load8(static_cast<const R*>(p.resid) + row + 8 * c, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += o[j];
+      }
+      if (p.resid_out) store8(static_cast<R*>(p.resid_out) + row + 8 * c, v[i]);
+    }
+    float wf[8];
+    unpack_bf16x8(w, wf);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss), v[i][j] *= wf[j];
+    if (p.codes) m[i] = half_warp_max(mag8(v[i]));
+  }
+  if (!p.y && !p.codes) return;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (kBlock) {
+    const int lane = t & 31;
+    if (lane == 0) part[t >> 5] = ss;
+    __syncthreads();
+    ss = lane < (lanes >> 5) ? part[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  }
+  // an infinite sum would turn the row's finite elements into zeros: the whole row is NaN instead
+  const float rms = ss < INFINITY ? rsqrtf(ss / float(p.d) + p.eps) : NAN;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = t + i * lanes;
+    if (c >= chunks) break;
+    if (p.codes) {
+      const uint32_t b = scale_byte(mag(__uint_as_float(m[i]) * rms));
+      *reinterpret_cast<uint2*>(p.codes + row + 8 * c) = code8(v[i], rms * scale_inverse(b));
+      if ((t & 15) == 0) p.scales[r * p.groups + (c >> 4)] = uint8_t(b);
+    }
+    if (p.y) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= rms;
+      store8(p.y + row + 8 * c, v[i]);
+    }
+  }
+}
+
+// A CTA per row.
 template <typename X, typename R, int CPT>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
   __shared__ float part[32];
   pdl_trigger();
   pdl_wait();
-  const int64_t row = int64_t(blockIdx.x) * p.d;
-  const int chunks = p.d >> 3, nt = blockDim.x;
-  float v[CPT][8];
-  uint4 w[CPT];  // the weights' loads are in flight with the row's
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int c = threadIdx.x + i * nt;
-    if (c < chunks) {
-      w[i] = __ldg(reinterpret_cast<const uint4*>(p.w + 8 * c));
-      load8(static_cast<const X*>(p.x) + row + 8 * c, v[i]);
-      if (p.resid) {
-        float r[8];
-        load8(static_cast<const R*>(p.resid) + row + 8 * c, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = nt >> 5;
-  if (lane == 0) part[warp] = ss;
-  __syncthreads();
-  ss = lane < nw ? part[lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  // an infinite sum would turn the row's finite elements into zeros: the whole row is NaN instead
-  const float rms = ss < INFINITY ? rsqrtf(ss / float(p.d) + p.eps) : NAN;
-#pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int c = threadIdx.x + i * nt;
-    const bool in = c < chunks;
-    if (in && p.resid_out) store8(static_cast<R*>(p.resid_out) + row + 8 * c, v[i]);
-    if (!p.y && !p.codes) continue;
-    if (in) {
-      float wf[8];
-      unpack_bf16x8(w[i], wf);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rms * wf[j];
-      if (p.y) store8(p.y + row + 8 * c, v[i]);
-    }
-    if (p.codes) {
-      const uint32_t b = scale_byte(half_warp_max(in ? mag8(v[i]) : 0u));
-      if (in) *reinterpret_cast<uint2*>(p.codes + row + 8 * c) = code8(v[i], scale_inverse(b));
-      if (in && (threadIdx.x & 15) == 0) p.scales[int64_t(blockIdx.x) * p.groups + (c >> 4)] = uint8_t(b);
-    }
-  }
+  norm_row<X, R, CPT, true>(p, blockIdx.x, threadIdx.x, blockDim.x, part);
+}
+
+// A warp per row, eight rows per CTA: no barrier.
+template <typename X, typename R, int CPT>
+__global__ void __launch_bounds__(256) rmsnorm_warp_kernel(const NormParams p, int T) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (r < T) norm_row<X, R, CPT, false>(p, r, threadIdx.x & 31, 32, nullptr);
 }
 
 template <typename X, typename R>
 cudaError_t launch_norm(const NormParams& p, int T, cudaStream_t s) {
   const int chunks = p.d >> 3;
-  const int cpt = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  // 16384 rows of 128 fp32: 7 us with a warp per row, 17 with a CTA
+  if (chunks <= 64) return launch_pdl(rmsnorm_warp_kernel<X, R, 2>, dim3((T + 7) / 8), dim3(256), 0, s, p, T);
+  // One chunk per thread is the quickest for few rows (1 x 4096 fp32: 2.2 us, 2.6 with two) and as good
+  // for many, except where a thread would read 16 bytes in all (16384 x 4096 bf16 without a residual: 66
+  // us, 54 with two) or the CTA have 1024 threads (8192 x 8192 bf16: 83 us, 80).
+  const int cpt = chunks > 2048 ? 4 : chunks > 512 || (chunks > 256 && sizeof(X) == 2 && !p.resid) ? 2 : 1;
   const int nt = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
   if (cpt == 1) return launch_pdl(rmsnorm_kernel<X, R, 1>, dim3(T), dim3(nt), 0, s, p);
   if (cpt == 2) return launch_pdl(rmsnorm_kernel<X, R, 2>, dim3(T), dim3(nt), 0, s, p);
