@@ -857,10 +857,10 @@ struct StreamPlan {
 
 // Tokens per tile: the accumulators (nw bn columns) and the scale words share 512 columns of tensor
 // memory, so 256 at most (208 for two matrices); narrower tiles give more CTAs, and tiles of up to
-// 128 / nw tokens can split K over a cluster.  The estimate is a fit to single launches: a wave costs
-// 2.4 us (5.5 with a cluster's exchange; more for tiles wider than 128 tokens) and, per block of K,
-// 0.2 + 0.0013 bn us (two matrices: 6.5 and 0.35 + 0.0035 bn), within 20% of what was measured from
-// 32 to 2048 tokens.
+// 128 / nw tokens can split K over a cluster.  The estimate is a fit to launches of 8 to 128 tiles of
+// 32 to 128 tokens, K = 2048 to 8192 (within 10%): a start that grows with the tile's tokens (they
+// pass the epilogue one warp each), with the cluster and with the share of the SMs in use, and a time
+// per block of K, which the issuing of its MMAs bounds up to 128 tokens.
 StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
   StreamPlan best{};
   for (int most : {256, 128, 64}) {
@@ -869,15 +869,21 @@ StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
     p.n_tiles = (N + 127) / 128, p.t_tiles = (T + most - 1) / most;
     p.bn = ((T + p.t_tiles - 1) / p.t_tiles + 15) / 16 * 16;
     const int64_t tiles = int64_t(p.n_tiles) * p.t_tiles;
-    // as many CTAs per tile as run at once (the sums of a wide tile would leave too little shared
-    // memory for the ring).  16 tiles of 64 tokens, K = 4096: 7.8 us with clusters of 6, 13.5 with
-    // clusters of 8, of which 15 fit.
-    p.splits = p.bn > 128 / nw ? 1 : std::min(8, KB);
-    while (p.splits > 1 && L->clusters[p.splits] < tiles) --p.splits;
-    const double waves = double((tiles * p.splits + L->sms - 1) / L->sms);
-    const double start = (p.splits > 1 ? (nw == 1 ? 5.5 : 6.5) : 2.4) + 0.032 * std::max(0, p.bn - 128);
-    p.us = waves * (start + (KB + p.splits - 1) / p.splits * (nw == 1 ? 0.2 + 0.0013 * p.bn : 0.35 + 0.0035 * p.bn));
-    if (!best.bn || p.us < best.us) best = p;
+    // (the sums of a wide tile would leave too little shared memory for the ring)
+    for (p.splits = 1; p.splits <= (p.bn > 128 / nw ? 1 : std::min(8, KB)); ++p.splits) {
+      // all clusters at once: 16 tiles of 64 tokens, K = 4096, take 6.8 us in clusters of 4 and 12.4 in
+      // clusters of 8, of which 15 fit
+      if (p.splits > 1 && L->clusters[p.splits] < tiles) break;
+      const int range = (KB + p.splits - 1) / p.splits;
+      const double waves = double((tiles * p.splits + L->sms - 1) / L->sms);
+      const double used = std::min(1.0, double(tiles * p.splits) / L->sms);
+      const double wide = std::max(0, p.bn - 128 / nw);
+      if (p.splits == 1)
+        p.us = waves * (2.0 + (nw == 1 ? 0.018 : 0.045) * p.bn + used + range * (nw == 1 ? 0.262 + 0.0015 * wide : 0.385 + 0.0012 * wide));
+      else
+        p.us = (nw == 1 ? 2.3 + 0.024 * p.bn : 2.9 + 0.043 * p.bn) + 0.08 * p.splits + 1.8 * used + range * (nw == 1 ? 0.245 : 0.37);
+      if (!best.bn || p.us < best.us) best = p;
+    }
   }
   return best;
 }
@@ -886,7 +892,7 @@ StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
 double pair_us(const scion_fp8* L, int nw, int T, int N, int KB) {
   const int64_t tiles = int64_t((T + 255) / 256) * (nw == 1 ? (N + 255) / 256 : (N + 127) / 128);
   const int pairs = std::max(1, L->sms / 2);
-  return (nw == 1 ? 4.5 : 5.4) + double((tiles + pairs - 1) / pairs) * (1.7 + 0.26 * KB);
+  return (nw == 1 ? 3.1 : 3.9) + double((tiles + pairs - 1) / pairs) * (1.0 + 0.33 * KB);
 }
 
 template <int NW>
@@ -917,10 +923,12 @@ int launch_stream(const scion_fp8* L, const StreamPlan& plan, StreamParams& p, c
 }
 
 // Up to 8 tokens, and up to 16 with few weights, run on mma.sync (k_fp8_rows.cu): it starts sooner, but
-// reads the tokens again for every 16 weight rows.  1 token, 8 MB of weights: 2.9 us against 5.2; 16
-// tokens: 8 MB 4.0 against 6.1, 22 MB 11.0 against 8.5, 67 MB 22.8 against 15.3.
+// reads the tokens again for every 16 weight rows.  2048 x 4096: 1 token 2.5 us against 4.9, 16 tokens
+// 3.6 against 5.3; 16 tokens, 4096 x 4096 5.4 against 7.0, 8192 x 8192 22.6 against 15.4; gated, 16
+// tokens, 2 x 2048 x 2048 6.4 against 6.7, 2 x 2048 x 5456 12.2 against 8.0.
 bool use_rows(const Call& c) {
-  return c.T <= 8 || (c.T <= 16 && int64_t(c.N) * c.K * (c.w[1] ? 2 : 1) <= (12 << 20));
+  const int64_t weights = int64_t(c.N) * c.K;
+  return c.T <= 8 || (c.T <= 16 && weights <= (c.w[1] ? 5 << 20 : 24 << 20));
 }
 
 template <int EPI>
