@@ -23,7 +23,7 @@ struct Call {
   uint8_t* codes;
   uint8_t* scales;
   int T, N, K, KB;  // KB = ceil(K / 128)
-  int out_bf16;
+  int out_bf16, sms;
 };
 
 // k_fp8_rows.cu: up to 16 tokens

@@ -924,7 +924,7 @@ int launch_stream(const scion_fp8* L, const StreamPlan& plan, StreamParams& p, c
 
 // Up to 8 tokens, and up to 16 with few weights, run on mma.sync (k_fp8_rows.cu): it starts sooner, but
 // reads the tokens again for every 16 weight rows.  2048 x 4096: 1 token 2.5 us against 4.9, 16 tokens
-// 3.6 against 5.3; 16 tokens, 4096 x 4096 5.4 against 7.0, 8192 x 8192 22.6 against 15.4; gated, 16
+// 3.5 against 5.3; 16 tokens, 4096 x 4096 5.4 against 7.0, 8192 x 8192 22.6 against 15.4; gated, 16
 // tokens, 2 x 2048 x 2048 6.4 against 6.7, 2 x 2048 x 5456 12.2 against 8.0.
 bool use_rows(const Call& c) {
   const int64_t weights = int64_t(c.N) * c.K;
@@ -951,7 +951,7 @@ Call call(const scion_fp8* L, const uint8_t* x, const uint8_t* sx, int T) {
   Call c{};
   c.x = x, c.sx = sx;
   c.w[0] = L->desc.w_codes, c.sw[0] = L->desc.w_scales, c.w[1] = L->desc.up_codes, c.sw[1] = L->desc.up_scales;
-  c.T = T, c.N = L->desc.n, c.K = L->desc.k, c.KB = (c.K + 127) / 128;
+  c.T = T, c.N = L->desc.n, c.K = L->desc.k, c.KB = (c.K + 127) / 128, c.sms = L->sms;
   return c;
 }
 

@@ -116,9 +116,9 @@ __device__ __forceinline__ void blocks(const Call& p, const Lane<NW, NT>& l, int
 }
 
 // NW matrices, NT tiles of 8 tokens, U blocks of K per warp with their loads in flight together, G:
-// results to 8 bits (gated, clusters of 8 CTAs)
-template <int NW, int NT, int U, bool G>
-__global__ void __launch_bounds__(kRowsWarps * 32, 2) fp8_rows_kernel(const Call p) {
+// results to 8 bits (gated, clusters of 8 CTAs); PerSm: CTAs whose registers fit an SM.
+template <int NW, int NT, int U, bool G, int PerSm>
+__global__ void __launch_bounds__(kRowsWarps * 32, PerSm) fp8_rows_kernel(const Call p) {
   __shared__ float part[kRowsWarps][NW][8 * NT][17];  // [warp][matrix][token][row], padded
   __shared__ uint32_t amax[8][8 * NT];                // [CTA of the cluster][token]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -192,20 +192,33 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 2) fp8_rows_kernel(const Call
   if (rank == 0 && r == 0) p.scales[int64_t(tok) * ((p.N + 127) / 128) + (blockIdx.x >> 3)] = uint8_t(b);
 }
 
-template <int NW, int NT, int U, bool G>
+template <int NW, int NT, int U, bool G, int PerSm>
 cudaError_t launch(const Call& c, cudaStream_t s) {
   const unsigned ctas = unsigned((c.N + 15) / 16);
   const dim3 block(kRowsWarps * 32);
-  if (G) return launch_pdl_cluster(fp8_rows_kernel<NW, NT, U, G>, dim3((ctas + 7) / 8 * 8), block, dim3(8), 0, s, c);
-  return launch_pdl(fp8_rows_kernel<NW, NT, U, G>, dim3(ctas), block, 0, s, c);
+  if (G) return launch_pdl_cluster(fp8_rows_kernel<NW, NT, U, G, PerSm>, dim3((ctas + 7) / 8 * 8), block, dim3(8), 0, s, c);
+  return launch_pdl(fp8_rows_kernel<NW, NT, U, G, PerSm>, dim3(ctas), block, 0, s, c);
 }
 
-// G: results to 8 bits.  U: a warp of a long row keeps 8 KB of weights in flight, which the weights of
-// a short one do not fill and which two tiles of tokens leave no registers for.
+// Registers against CTAs.  Where every SM has one CTA at most, its warps take the registers to keep a
+// whole row's blocks in flight; where there are many, more CTAs per SM keep more loads in flight than
+// deeper ones.  One token, n x k (us): 2048 x 4096 (128 CTAs) U = 4 with registers for one CTA per SM 2.9,
+// for two 3.9; 4096 x 4096 (256) 4.8, 4.0, U = 2 3.7; 8192 x 8192 (512) U = 4 for two 15.9, U = 2 for four
+// 13.9.  16 tokens: 2048 x 4096 U = 2 for one 3.7, for two 4.6; 4096 x 4096 6.6, U = 1 5.4.
 template <int NW, bool G>
 cudaError_t launch_tokens(const Call& c, cudaStream_t s) {
-  if (c.T > 8) return launch<NW, 2, 2 / NW, G>(c, s);
-  return c.KB > 2 * kRowsWarps ? launch<NW, 1, 4 / NW, G>(c, s) : launch<NW, 1, 2 / NW, G>(c, s);
+  const int ctas = (c.N + 15) / 16;
+  const bool few = ctas <= c.sms, longer = c.KB > 2 * kRowsWarps;
+  if constexpr (NW == 1) {
+    if (c.T > 8) return few ? launch<1, 2, 2, G, 1>(c, s) : launch<1, 2, 1, G, 2>(c, s);
+    if (few && longer) return launch<1, 1, 4, G, 1>(c, s);
+    return ctas <= 2 * c.sms ? launch<1, 1, 2, G, 2>(c, s) : launch<1, 1, 2, G, 4>(c, s);
+  } else {
+    // With one CTA per SM, clusters of 8 CTAs fill little more than three quarters of the SMs.  16 tokens,
+    // 2 x 1024 x 4096 (64 CTAs): one per SM 6.2, two (which spills 136 bytes) 7.8; 2 x 2048 x 2048 (128) 7.8, 6.5.
+    if (c.T > 8) return ctas <= c.sms * 3 / 4 ? launch<2, 2, 1, G, 1>(c, s) : launch<2, 2, 1, G, 2>(c, s);
+    return longer && !few ? launch<2, 1, 2, G, 2>(c, s) : launch<2, 1, 1, G, 2>(c, s);
+  }
 }
 
 }  // namespace
