@@ -51,8 +51,7 @@ struct NormParams {
 // The row of `lanes` threads (a warp, or the whole CTA with kBlock): thread t of them holds the 8-column
 // chunks t, t + lanes, ..., so that the row stays in registers between the statistic and the output.
 // y = (r w) rms: the products r w and their largest magnitude per group do not wait for the statistic,
-// and (rounding is monotonic, a scale a power of two) max |y| = max |r w| rms and y / s = (r w)(rms / s)
-// to the last bit.
+// and (rounding is monotonic) max |y| = max |r w| rms to the last bit.
 template <typename X, typename R, int CPT, bool kBlock>
 __device__ __forceinline__ void norm_row(const NormParams& p, int64_t r, int t, int lanes, float* part) {
   const int64_t row = r * p.d;
@@ -101,16 +100,15 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t r, int t, 
   for (int i = 0; i < CPT; ++i) {
     const int c = t + i * lanes;
     if (c >= chunks) break;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] *= rms;
     if (p.codes) {
+      // (in two steps: near the smallest numbers rms / s leaves the fp32 range where y / s does not)
       const uint32_t b = scale_byte(mag(__uint_as_float(m[i]) * rms));
-      *reinterpret_cast<uint2*>(p.codes + row + 8 * c) = code8(v[i], rms * scale_inverse(b));
+      *reinterpret_cast<uint2*>(p.codes + row + 8 * c) = code8(v[i], scale_inverse(b));
       if ((t & 15) == 0) p.scales[r * p.groups + (c >> 4)] = uint8_t(b);
     }
-    if (p.y) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= rms;
-      store8(p.y + row + 8 * c, v[i]);
-    }
+    if (p.y) store8(p.y + row + 8 * c, v[i]);
   }
 }
 

@@ -162,6 +162,27 @@ def test_norm_special_rows():
     assert torch.isfinite(y[keep]).all()
 
 
+@pytest.mark.parametrize("d", [272, 2048])
+@pytest.mark.parametrize("size", [1e-34, 1e-36, 3e-38, 1e-40])
+def test_norm_of_rows_near_the_smallest_numbers(d, size):
+    """The statistic is eps alone and the scale's inverse near the end of the fp32 range."""
+    T = 3
+    x, _, w = norm_case(T, d, F32, None)
+    x = (x.double() * size).float()
+    x[1, ::3] = 0
+    y = torch.empty((T, d), dtype=BF16, device=DEV)
+    codes = torch.empty((T, d), dtype=torch.uint8, device=DEV)
+    scales = torch.empty((T, -(-d // 128)), dtype=torch.uint8, device=DEV)
+    tq.scion_rmsnorm_forward(x.to(DEV), T, w.to(DEV), 1e-6, y=y, y_codes=codes, y_scales=scales)
+    _, ry = R.rmsnorm(host(x), None, host(w), 1e-6)
+    # as in check_norm, and below the smallest normal number 2^-150 per fp32 product: r w (then times
+    # 10^3 = 1 / sqrt(eps)) and y
+    err = np.abs(ry) * ((d + 4) / 2 + 9) * 2.0 ** -24 + 2.0 ** -150 * 1001
+    # (a bf16 below 2^-126 is off by 2^-134 at most)
+    assert (np.abs(host(y) - ry) <= np.abs(ry) * 2.0 ** -8 + 2.0 ** -134 + 2 * err).all()
+    R.check_codes(bytes_of(codes), bytes_of(scales), ry, err)
+
+
 # ------------------------------------------------------------------ products
 def quantized(rng, rows, cols, block_rows, std=1.0):
     v = activations(rng, rows, cols) * std
