@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
     bool ok = true;
     const uint32_t low0 = umma_desc_low(ring), sf_step = 4 * NW + p.sfb_cols;
     uint32_t low = low0, accumulate = 0;
+    pdl_wait();  // (so that the limits of the waits below count from the predecessor's end)
     for (int kb = kb0; kb < kb1; kb += kStageBlocks<NW>) {
       ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * at.slot, at.parity, abort_flag, p.err));
 #pragma unroll
