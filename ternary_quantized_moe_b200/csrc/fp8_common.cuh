@@ -26,7 +26,7 @@ struct Call {
   int out_bf16, sms;
 };
 
-// k_fp8_rows.cu: up to 16 tokens
+// k_fp8_rows.cu: up to 32 tokens
 cudaError_t launch_rows(const Call& c, cudaStream_t s);
 
 // |v| as an unsigned integer: ordered like the magnitudes, infinities and NaN above every number

@@ -923,13 +923,18 @@ int launch_stream(const scion_fp8* L, const StreamPlan& plan, StreamParams& p, c
                                    dim3(splits, 1, 1), smem, s, p));
 }
 
-// Up to 8 tokens, and up to 16 with few weights, run on mma.sync (k_fp8_rows.cu): it starts sooner, but
-// reads the tokens again for every 16 weight rows.  2048 x 4096: 1 token 2.5 us against 4.9, 16 tokens
-// 3.5 against 5.3; 16 tokens, 4096 x 4096 5.4 against 7.0, 8192 x 8192 22.6 against 15.4; gated, 16
-// tokens, 2 x 2048 x 2048 6.4 against 6.7, 2 x 2048 x 5456 12.2 against 8.0.
+// Up to 8 tokens, and up to 16 or 32 with few weights, run on mma.sync (k_fp8_rows.cu): it starts sooner,
+// but reads the tokens again for every 16 weight rows and its products are slower (about 50 cycles per
+// step of 8 tokens x 16 rows x 32 columns).  n x k, us against the stream kernel: 2048 x 4096, 1 token 2.8
+// against 4.9, 16 tokens 3.6 against 5.3; 16 tokens, 4096 x 4096 5.4 against 7.0, 8192 x 8192 22.6 against
+// 15.4; 32 tokens, 2048 x 2048 3.7 against 5.4, 4096 x 2048 5.4 against 5.9, 2048 x 4096 5.6 against 6.1,
+// 1024 x 8192 9.5 against 6.7, 4096 x 4096 8.4 against 7.2.  Gated, 16 tokens, 2 x 2048 x 2048 6.4 against
+// 6.7, 2 x 2048 x 5456 12.2 against 8.0; 32 tokens, 2 x 512 x 2048 6.2 against 6.0.
 bool use_rows(const Call& c) {
   const int64_t weights = int64_t(c.N) * c.K;
-  return c.T <= 8 || (c.T <= 16 && weights <= (c.w[1] ? 5 << 20 : 24 << 20));
+  if (c.T <= 8) return true;
+  if (c.w[1]) return c.T <= 16 && weights <= 5 << 20;
+  return c.T <= 16 ? weights <= 24 << 20 : c.T <= 32 && c.K <= 4096 && weights <= 8 << 20;
 }
 
 template <int EPI>

@@ -1,5 +1,5 @@
 // k_fp8_rows.cu -- products in e4m3 with power-of-two block scales for single tokens and small decode
-// batches (up to 16 tokens).
+// batches (up to 32 tokens).
 //
 // Bound by latency and by reading the weights once, so the path from the first load to the result is
 // kept short: no ring, no tensor memory, no cluster for a plain layer.  A CTA holds 16 weight rows (of
@@ -151,45 +151,56 @@ __global__ void __launch_bounds__(kRowsWarps * 32, PerSm) fp8_rows_kernel(const 
 #pragma unroll
       for (int i = 0; i < 4; ++i) part[warp][m][8 * t + 2 * c + (i & 1)][g + 8 * (i >> 1)] = acc[m][t][i];
   __syncthreads();
-  // thread: row threadIdx % 16 of token threadIdx / 16 (a half warp per token)
-  const int r = threadIdx.x & 15, tok = threadIdx.x >> 4, n = row0 + r;
-  const bool mine = tok < 8 * NT && tok < p.T && n < p.N;
-  float v[NW];
-#pragma unroll
-  for (int m = 0; m < NW; ++m) {
-    v[m] = 0.f;
-    if (tok < 8 * NT)
-#pragma unroll
-      for (int w = 0; w < kRowsWarps; ++w) v[m] += part[w][m][tok][r];
-  }
-  const int64_t at = int64_t(tok) * p.N + n;
-  if (NW == 1) {
-    if (!mine) return;
-    if (p.base) v[0] += p.base[at];
-    if (p.out_bf16) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(v[0]);
-    else static_cast<float*>(p.out)[at] = v[0];
-    return;
-  }
-  const float h = silu_mul(v[0], v[NW - 1]);
-  if (!G) {
-    if (mine) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(h);
-    return;
-  }
+  // thread: row threadIdx % 16 of tokens threadIdx / 16, 16 further, ... (a half warp per token)
+  constexpr int kPasses = (NT + 1) / 2;
+  const int r = threadIdx.x & 15, tok0 = threadIdx.x >> 4, n = row0 + r;
   const uint32_t half = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
-  const uint32_t m = __reduce_max_sync(half, mine ? mag(h) : 0u);
   const int rank = blockIdx.x & 7;
-  if (tok < 8 * NT && r < 8) {  // one magnitude per token to each CTA of the cluster
-    const uint32_t dst = map_cluster_rank(smem_addr(&amax[rank][tok]), r);
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst), "r"(m) : "memory");
-  }
-  cluster_sync();
-  if (!mine) return;
-  uint32_t top = 0;
+  float h[kPasses];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, amax[i][tok]);
-  const uint32_t b = scale_byte(top);
-  p.codes[at] = uint8_t(pack4(h * scale_inverse(b), 0.f, 0.f, 0.f));
-  if (rank == 0 && r == 0) p.scales[int64_t(tok) * ((p.N + 127) / 128) + (blockIdx.x >> 3)] = uint8_t(b);
+  for (int i = 0; i < kPasses; ++i) {
+    const int tok = tok0 + 16 * i;
+    const bool mine = tok < p.T && n < p.N;
+    float v[NW];
+#pragma unroll
+    for (int m = 0; m < NW; ++m) {
+      v[m] = 0.f;
+      if (tok < 8 * NT)
+#pragma unroll
+        for (int w = 0; w < kRowsWarps; ++w) v[m] += part[w][m][tok][r];
+    }
+    const int64_t at = int64_t(tok) * p.N + n;
+    if (NW == 1) {
+      if (!mine) continue;
+      if (p.base) v[0] += p.base[at];
+      if (p.out_bf16) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(v[0]);
+      else static_cast<float*>(p.out)[at] = v[0];
+      continue;
+    }
+    h[i] = silu_mul(v[0], v[NW - 1]);
+    if (!G) {
+      if (mine) static_cast<bf16*>(p.out)[at] = __float2bfloat16_rn(h[i]);
+      continue;
+    }
+    const uint32_t m = __reduce_max_sync(half, mine ? mag(h[i]) : 0u);
+    if (tok < 8 * NT && r < 8) {  // one magnitude per token to each CTA of the cluster
+      const uint32_t dst = map_cluster_rank(smem_addr(&amax[rank][tok]), r);
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst), "r"(m) : "memory");
+    }
+  }
+  if (!G) return;
+  cluster_sync();
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int tok = tok0 + 16 * i;
+    if (tok >= p.T || n >= p.N) return;
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, amax[j][tok]);
+    const uint32_t b = scale_byte(top);
+    p.codes[int64_t(tok) * p.N + n] = uint8_t(pack4(h[i] * scale_inverse(b), 0.f, 0.f, 0.f));
+    if (rank == 0 && r == 0) p.scales[int64_t(tok) * ((p.N + 127) / 128) + (blockIdx.x >> 3)] = uint8_t(b);
+  }
 }
 
 template <int NW, int NT, int U, bool G, int PerSm>
@@ -204,12 +215,14 @@ cudaError_t launch(const Call& c, cudaStream_t s) {
 // whole row's blocks in flight; where there are many, more CTAs per SM keep more loads in flight than
 // deeper ones.  One token, n x k (us): 2048 x 4096 (128 CTAs) U = 4 with registers for one CTA per SM 2.9,
 // for two 3.9; 4096 x 4096 (256) 4.8, 4.0, U = 2 3.7; 8192 x 8192 (512) U = 4 for two 15.9, U = 2 for four
-// 13.9.  16 tokens: 2048 x 4096 U = 2 for one 3.7, for two 4.6; 4096 x 4096 6.6, U = 1 5.4.
+// 13.9.  16 tokens: 2048 x 4096 U = 2 for one 3.7, for two 4.6; 4096 x 4096 6.6, U = 1 5.4.  32 tokens (U =
+// 1): 2048 x 2048 for one 3.7, for two 5.1; 4096 x 2048 6.6, 5.4.
 template <int NW, bool G>
 cudaError_t launch_tokens(const Call& c, cudaStream_t s) {
   const int ctas = (c.N + 15) / 16;
   const bool few = ctas <= c.sms, longer = c.KB > 2 * kRowsWarps;
   if constexpr (NW == 1) {
+    if (c.T > 16) return few ? launch<1, 4, 1, G, 1>(c, s) : launch<1, 4, 1, G, 2>(c, s);
     if (c.T > 8) return few ? launch<1, 2, 2, G, 1>(c, s) : launch<1, 2, 1, G, 2>(c, s);
     if (few && longer) return launch<1, 1, 4, G, 1>(c, s);
     return ctas <= 2 * c.sms ? launch<1, 1, 2, G, 2>(c, s) : launch<1, 1, 2, G, 4>(c, s);

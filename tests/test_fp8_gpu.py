@@ -244,6 +244,29 @@ def test_linear(T, K, N):
     c.check(inplace, c.base)
 
 
+@pytest.mark.parametrize("T,K,N", [(1, 4112, 1000), (8, 4112, 2390), (3, 2064, 4800), (5, 272, 5000), (12, 2064, 2000),
+                                   (16, 4112, 2390), (17, 144, 100), (24, 2064, 2000), (25, 2048, 2391), (31, 4096, 1000),
+                                   (32, 4096, 2048), (32, 4112, 264)])
+def test_linear_few_tokens(T, K, N):
+    """Batches of up to 32 tokens: few and many weight rows, K of one round of blocks and more."""
+    c = Case(T, K, N)
+    for out_type in (F32, BF16):
+        c.check(c.run(out_type, torch.from_numpy(c.base).to(DEV)), c.base)
+
+
+@pytest.mark.parametrize("T,K,F", [(2, 4112, 2400), (8, 2064, 2400), (12, 4112, 1008), (16, 2064, 2000), (24, 2064, 400)])
+def test_gated_few_tokens(T, K, F):
+    c = Case(T, K, F, gated=True)
+    ref, err = gated_reference(c)
+    codes = torch.empty((T, F), dtype=torch.uint8, device=DEV)
+    scales = torch.empty((T, -(-F // 128)), dtype=torch.uint8, device=DEV)
+    tq.scion_fp8_gated_forward(c.dx, c.dsx, T, c.layer, h_codes=codes, h_scales=scales)
+    R.check_codes(bytes_of(codes), bytes_of(scales), ref, err)
+    h = torch.empty((T, F), dtype=BF16, device=DEV)
+    tq.scion_fp8_gated_forward(c.dx, c.dsx, T, c.layer, h=h)
+    assert (np.abs(host(h) - ref) <= np.abs(ref) * 2.0 ** -8 + 2 * err).all()
+
+
 @pytest.mark.parametrize("T", [3, 70, 400])
 def test_linear_is_reproducible_and_rows_are_independent(T):
     c = Case(T, 2048, 640)
