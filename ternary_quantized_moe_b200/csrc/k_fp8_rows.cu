@@ -10,6 +10,8 @@
 // two) and added in fp32; the warps' sums meet in shared memory and are added in warp order.
 // A gated layer that writes 8 bits needs the largest |h| of 128 features: the eight CTAs of a cluster
 // hold them and exchange one magnitude per token.
+// Measured (replayed from a graph, one token): 4096 x 2048 2.5 us, 16384 x 8192 25.5 us (5.3 TB/s), gated
+// 2 x 512 x 2048 3.1 us; 8 tokens, gated 2 x 8192 x 4096 15.5 us (4.3 TB/s).
 #include "fp8_common.cuh"
 #include "scion_internal.cuh"
 

@@ -5,7 +5,10 @@
 // memory in between.  A thread holds 8 consecutive columns (16 bytes of bf16, 32 of fp32 per load
 // and lane), so a group of 128 columns is half a warp and its largest magnitude one redux over 16
 // lanes; the loads of a warp cover whole 32-byte sectors.  Programmatic dependent launch lets a call's
-// blocks start as its predecessor's drain.
+// blocks start as its predecessor's drain.  Replayed from a graph: the norm of 16384 x 4096 (bf16 + fp32
+// in, fp32 + 8 bits out, 738 MB) 106.7 us, 6.9 TB/s, and of one row of 2048 1.8 us; 8192 x 8192 fp32 in
+// 128 x 128 blocks 49.3 us, 6.8 TB/s; 16384 x 4096 bf16 by rows 37.3 us, 5.4 TB/s (issue slots 84% busy:
+// the conversions of two bytes of source to one).
 #include <math.h>
 
 #include <algorithm>
@@ -184,7 +187,7 @@ struct Chunk<bf16> {
 
 // Activations: a half warp per group of 128 columns of a row, `per` rows per CTA, four groups' loads
 // in flight.  (With a division per group to find its row the kernel was bound by its instructions:
-// 16384 x 4096 bf16 in 52 us with a 64-bit one, 42 us with a 32-bit one.)
+// 16384 x 4096 bf16 in 52 us with a 64-bit one, 42 us with a 32-bit one, 37 us without.)
 template <typename S>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const S* __restrict__ src, int64_t rows, int cols, int groups,
                                                             int per, uint8_t* __restrict__ codes,
