@@ -513,7 +513,7 @@ struct PairBars {
   uint32_t amax[2][2][128];  // [tile parity][column half][token]
 };
 
-enum PairEpi { kPairBf16 = 0, kPairF32 = 1, kPairBase = 2, kPairGatedBf16 = 3, kPairGatedCodes = 4 };
+enum PairEpi { kPairBf16 = 0, kPairF32 = 1, kPairBase = 2, kPairGatedBf16 = 3, kPairGatedCodes = 4, kPairLoose = 5 };
 
 __device__ __forceinline__ void pair_tile(const PairParams& p, int i, int& mt, int& nt) {
   const int per = kPairGroup * p.n_tiles, g = i / per, r = i - g * per;
@@ -578,6 +578,33 @@ __device__ __forceinline__ void store_rows(const RowsOut& o, const uint32_t (&v)
     }
     __syncwarp();
     if (c + 1 < 128 / kCols) load_base<kBase>(o, c + 1, lane, b);
+  }
+}
+
+// The same for rows of any alignment: a row of a chunk (32 columns) per instruction, one element per lane.
+// All of a chunk's base is in flight at once.
+__device__ __forceinline__ void store_rows_loose(const RowsOut& o, const uint32_t (&v)[128], uint32_t stage, int lane) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int n = o.n0 + 32 * c + lane;
+    const int rows = n < o.N ? int(min(int64_t(32), o.T - o.tok)) : 0;
+    const int64_t at = o.tok * o.N + n;
+    float b[32];
+#pragma unroll
+    for (int r = 0; r < 32; ++r) b[r] = o.base && r < rows ? o.base[at + int64_t(r) * o.N] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      sts_v4(stage + lane * 128 + ((i ^ (lane & 7)) << 4), v[32 * c + 4 * i], v[32 * c + 4 * i + 1], v[32 * c + 4 * i + 2],
+             v[32 * c + 4 * i + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const float x = lds_f32(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) + b[r];
+      if (r >= rows) continue;
+      if (o.out_bf16) reinterpret_cast<bf16*>(o.out)[at + int64_t(r) * o.N] = __float2bfloat16_rn(x);
+      else reinterpret_cast<float*>(o.out)[at + int64_t(r) * o.N] = x;
+    }
+    __syncwarp();
   }
 }
 
@@ -769,7 +796,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       if (lane == 0) mbar_arrive_remote_relaxed(released);
       const int64_t tok = int64_t(mt) * 256 + rank * 128 + row;
       const bool live = tok < p.T;
-      if (!kGated) {
+      if (EPI == kPairLoose) {
+        store_rows_loose(rows, v, staging + (warp - 8) * 4096, lane);
+      } else if (!kGated) {
         store_rows<EPI == kPairBf16 ? 2 : 4, EPI == kPairBase>(rows, v, staging + (warp - 8) * 4096, lane, base);
       } else {
         const int f0 = nt * 128 + half * 64;
@@ -1006,7 +1035,8 @@ extern "C" int scion_fp8_create(const scion_fp8_desc* D, void* stream, scion_fp8
   for (const auto f : {scion::fp8_stream_kernel<1>, scion::fp8_stream_kernel<2>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, scion::kSmem);
   for (const auto f : {scion::fp8_pair_kernel<scion::kPairBf16>, scion::fp8_pair_kernel<scion::kPairF32>,
-                       scion::fp8_pair_kernel<scion::kPairBase>, scion::fp8_pair_kernel<scion::kPairGatedBf16>, scion::fp8_pair_kernel<scion::kPairGatedCodes>})
+                       scion::fp8_pair_kernel<scion::kPairBase>, scion::fp8_pair_kernel<scion::kPairLoose>,
+                       scion::fp8_pair_kernel<scion::kPairGatedBf16>, scion::fp8_pair_kernel<scion::kPairGatedCodes>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, scion::kSmem);
   for (int n = 1; n <= 8 && e == cudaSuccess; ++n) e = scion::max_clusters(n, &L->clusters[n]);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&L->err), sizeof(int));
@@ -1046,8 +1076,9 @@ extern "C" int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales
   p.vec = p.N % 4 == 0 && !scion::fp8::misaligned(base, 16) && !scion::fp8::misaligned(out, 16);
   const bool rows16 = int64_t(p.N) * (p.out_bf16 ? 2 : 4) % 16 == 0 && p.vec;
   const scion::StreamPlan plan = scion::plan_stream(L, 1, T, p.N, p.KB);
-  if (rows16 && scion::pair_us(L, 1, T, p.N, p.KB) < plan.us)  // (it stores 16-byte pieces of rows)
-    return base         ? scion::launch_pair<scion::kPairBase>(L, p, x_codes, T, s)
+  if (scion::pair_us(L, 1, T, p.N, p.KB) < plan.us)
+    return !rows16      ? scion::launch_pair<scion::kPairLoose>(L, p, x_codes, T, s)
+           : base       ? scion::launch_pair<scion::kPairBase>(L, p, x_codes, T, s)
            : p.out_bf16 ? scion::launch_pair<scion::kPairBf16>(L, p, x_codes, T, s)
                         : scion::launch_pair<scion::kPairF32>(L, p, x_codes, T, s);
   return scion::launch_stream<1>(L, plan, p, x_codes, T, s);

@@ -137,7 +137,7 @@ template <typename X, typename R>
 cudaError_t launch_norm(const NormParams& p, int T, cudaStream_t s) {
   const int chunks = p.d >> 3;
   // 16384 rows of 128 fp32: 7 us with a warp per row, 17 with a CTA
-  if (chunks <= 64) return launch_pdl(rmsnorm_warp_kernel<X, R, 2>, dim3((T + 7) / 8), dim3(256), 0, s, p, T);
+  if (chunks <= 64) return launch_pdl(rmsnorm_warp_kernel<X, R, 2>, dim3(unsigned((int64_t(T) + 7) / 8)), dim3(256), 0, s, p, T);
   // One chunk per thread is the quickest for few rows (1 x 4096 fp32: 2.2 us, 2.6 with two) and as good
   // for many, except where a thread would read 16 bytes in all (16384 x 4096 bf16 without a residual: 66
   // us, 54 with two) or the CTA have 1024 threads (8192 x 8192 bf16: 83 us, 80).

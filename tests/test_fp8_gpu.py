@@ -324,6 +324,26 @@ def test_linear_unaligned(T, K, N):
         assert buf[0] == 7 and buf[-1] == 7
 
 
+@pytest.mark.parametrize("T,K,N", [(700, 2064, 2303), (1100, 640, 4100), (2600, 640, 1041), (2049, 272, 2306), (3000, 2048, 300)])
+def test_linear_many_tokens_unaligned_rows(T, K, N):
+    """Rows of outputs and bases at every alignment, in many tiles; in place; nothing beside them written."""
+    c = Case(T, K, N)
+    for out_type in (F32, BF16):
+        buf = torch.full((T * N + 2,), 7.0, dtype=out_type, device=DEV)
+        out = buf[1:-1].view(T, N)
+        tq.scion_fp8_forward(c.dx, c.dsx, T, c.layer, out)
+        c.check(out)
+        tq.scion_fp8_forward(c.dx, c.dsx, T, c.layer, out, base=torch.from_numpy(c.base).to(DEV))
+        c.check(out, c.base)
+        assert buf[0] == 7 and buf[-1] == 7
+    buf = torch.full((T * N + 2,), 7.0, dtype=F32, device=DEV)
+    out = buf[1:-1].view(T, N)
+    out.copy_(torch.from_numpy(c.base))
+    tq.scion_fp8_forward(c.dx, c.dsx, T, c.layer, out, base=out)
+    c.check(out, c.base)
+    assert buf[0] == 7 and buf[-1] == 7 and tq.scion_fp8_check(c.layer) == 0
+
+
 GATED = [(1, 16, 16), (1, 2048, 512), (2, 128, 128), (7, 144, 112), (16, 512, 144), (33, 2048, 272), (50, 2048, 528),
          (64, 4112, 384), (65, 256, 1008), (100, 2064, 256), (129, 1024, 240), (257, 512, 528), (300, 2048, 512),
          (1025, 1024, 768), (600, 16, 16), (2600, 640, 1040)]
