@@ -581,28 +581,43 @@ __device__ __forceinline__ void store_rows(const RowsOut& o, const uint32_t (&v)
   }
 }
 
-// The same for rows of any alignment: a row of a chunk (32 columns) per instruction, one element per lane.
-// All of a chunk's base is in flight at once.
+// The same for rows of any alignment: 32 columns of a row per instruction, one element per lane.  Bound by
+// its instructions, so that a row costs a load from shared memory at a constant offset, a pointer's step
+// and a store (4096 x 4095 fp32, K = 512: 60 us with pieces that start on a line and indexes per element).
+template <typename Out>
 __device__ __forceinline__ void store_rows_loose(const RowsOut& o, const uint32_t (&v)[128], uint32_t stage, int lane) {
+  constexpr int kRows = 16;
+  uint32_t from[8];  // the lane's column of rows r, r + 8, ...
+#pragma unroll
+  for (int r = 0; r < 8; ++r) from[r] = stage + r * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4;
+  const int all = int(min(int64_t(32), o.T - o.tok));
+  const int64_t step = o.N;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int n = o.n0 + 32 * c + lane;
-    const int rows = n < o.N ? int(min(int64_t(32), o.T - o.tok)) : 0;
-    const int64_t at = o.tok * o.N + n;
-    float b[32];
-#pragma unroll
-    for (int r = 0; r < 32; ++r) b[r] = o.base && r < rows ? o.base[at + int64_t(r) * o.N] : 0.f;
+    const int rows = n < o.N ? all : 0;
+    Out* dst = reinterpret_cast<Out*>(o.out) + o.tok * step + n;
+    const float* src = o.base + o.tok * step + n;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       sts_v4(stage + lane * 128 + ((i ^ (lane & 7)) << 4), v[32 * c + 4 * i], v[32 * c + 4 * i + 1], v[32 * c + 4 * i + 2],
              v[32 * c + 4 * i + 3]);
     __syncwarp();
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += kRows) {
+      float x[kRows];
+      if (o.base) {
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      const float x = lds_f32(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) + b[r];
-      if (r >= rows) continue;
-      if (o.out_bf16) reinterpret_cast<bf16*>(o.out)[at + int64_t(r) * o.N] = __float2bfloat16_rn(x);
-      else reinterpret_cast<float*>(o.out)[at + int64_t(r) * o.N] = x;
+        for (int r = 0; r < kRows; ++r, src += step) x[r] = r0 + r < rows ? *src : 0.f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) x[r] += lds_f32(from[r & 7] + (r0 + r / 8 * 8) * 128);
+      } else {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) x[r] = lds_f32(from[r & 7] + (r0 + r / 8 * 8) * 128);
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r, dst += step)
+        if (r0 + r < rows) *dst = Out(x[r]);
     }
     __syncwarp();
   }
@@ -797,7 +812,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       const int64_t tok = int64_t(mt) * 256 + rank * 128 + row;
       const bool live = tok < p.T;
       if (EPI == kPairLoose) {
-        store_rows_loose(rows, v, staging + (warp - 8) * 4096, lane);
+        if (p.out_bf16) store_rows_loose<bf16>(rows, v, staging + (warp - 8) * 4096, lane);
+        else store_rows_loose<float>(rows, v, staging + (warp - 8) * 4096, lane);
       } else if (!kGated) {
         store_rows<EPI == kPairBf16 ? 2 : 4, EPI == kPairBase>(rows, v, staging + (warp - 8) * 4096, lane, base);
       } else {
