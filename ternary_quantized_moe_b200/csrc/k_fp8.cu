@@ -53,7 +53,7 @@ constexpr int kStageBlocks = 2 / NW;
 constexpr int kSfSlots = 4;  // ring of scale words, each slot for 4 K blocks (one byte each)
 constexpr uint32_t kNoScale = 0x7f7f7f7fu;  // words of rows past the end: 2^0
 constexpr uint32_t kSmem = 227 * 1024;
-constexpr int kMaxTokens = 1 << 21;  // token tiles stay within a grid's z, tiles within 32 bits
+constexpr int kMaxTokens = 1 << 21;  // token tiles stay within a grid's z, tiles and scale bytes within 32 bits
 
 struct StreamParams {
   CUtensorMap w[2], x;
@@ -75,40 +75,67 @@ struct Bars {
   int abort_flag;
 };
 
-// Scale bytes of an array [rows][KB]: its first byte and its end.
+// Scale bytes of an array [rows][KB] (fewer than 2^31) as aligned words: byte i of the array is byte
+// i + off from `base`, a multiple of 4; words lo .. hi - 1 lie in the array, and what it has of the words
+// on either side of them is in head and tail.
 struct Scales {
-  const uint8_t* first;
-  const uint8_t* end;
+  const uint8_t* base;
+  int off, lo, hi;
+  uint32_t head, tail;
 };
 
-// The aligned word at `a`: what of it lies in the array.
-__device__ __forceinline__ uint32_t word_inside(const uint8_t* a, const Scales& s) {
-  if (a >= s.first && a + 4 <= s.end) return *reinterpret_cast<const uint32_t*>(a);
-  uint32_t w = 0;
-  for (int j = 0; j < 4; ++j)
-    if (a + j >= s.first && a + j < s.end) w |= uint32_t(a[j]) << (8 * j);
-  return w;
+__device__ __forceinline__ Scales scales_of(const uint8_t* first, int n, int align) {
+  Scales s;
+  s.off = int(reinterpret_cast<uintptr_t>(first) & 3);
+  s.base = first - s.off;
+  n += s.off;
+  s.lo = (s.off + 3) >> 2, s.hi = n >> 2;
+  s.head = s.tail = 0;
+  if (align == 1) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      if (j + 1 >= s.off && j + 1 < n && s.lo) s.head |= uint32_t(s.base[j + 1]) << (8 * j + 8);
+      if (j < (n & 3) && 4 * s.hi + j >= s.off) s.tail |= uint32_t(s.base[4 * s.hi + j]) << (8 * j);
+    }
+  }
+  return s;
 }
 
 // Scale bytes of one row are read 16 K blocks at a time (a "round": four words of four blocks), so
 // that the loads of a round overlap and the next round's are in flight while the MMAs use this one.
-// `align`: alignment of the row starts (16, 4 or 1).  Bytes of blocks past the row's end are whatever
+// `align`: alignment of the row starts (16 or 4).  Bytes of blocks past the row's end are whatever
 // follows in the array; no MMA selects them.
-__device__ __forceinline__ uint4 scale_round(const Scales& s, int64_t row, int r, int KB, int align) {
-  const uint8_t* p = s.first + row * KB + 16 * r;
+__device__ __forceinline__ uint4 scale_round(const Scales& s, int row, int r, int KB, int align) {
+  const uint8_t* p = s.base + row * KB + 16 * r;
   if (align == 16) return *reinterpret_cast<const uint4*>(p);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = 16 * r + 4 * i < KB ? *reinterpret_cast<const uint32_t*>(p + 4 * i) : kNoScale;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Row starts of any alignment: five words around the sixteen bytes, all of a round's rows loaded before
+// the first is shifted into place (a load and its use row by row made every call 1 to 2 us longer).
+struct ScaleWords {
   uint32_t w[5];
-  if (align == 4) {
+};
+__device__ __forceinline__ ScaleWords scale_words(const Scales& s, int row, int r, int KB) {
+  const int at = (s.off + row * KB + 16 * r) >> 2;
+  ScaleWords v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = 16 * r + 4 * i < KB ? *reinterpret_cast<const uint32_t*>(p + 4 * i) : kNoScale;
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 5; ++i) {
+    v.w[i] = 0;
+    if (s.lo < s.hi) v.w[i] = *reinterpret_cast<const uint32_t*>(s.base + 4 * min(max(at + i, s.lo), s.hi - 1));
   }
-  // five aligned words around the sixteen bytes, shifted into place
-  const int off = int(reinterpret_cast<uintptr_t>(p) & 3);
+  return v;
+}
+__device__ __forceinline__ uint4 scale_round(const Scales& s, int row, int r, int KB, const ScaleWords& v) {
+  const int at = s.off + row * KB + 16 * r, shift = 8 * (at & 3);
+  uint32_t w[5];
 #pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = word_inside(p - off + 4 * i, s);
-  return make_uint4(__funnelshift_r(w[0], w[1], 8 * off), __funnelshift_r(w[1], w[2], 8 * off),
-                    __funnelshift_r(w[2], w[3], 8 * off), __funnelshift_r(w[3], w[4], 8 * off));
+  for (int i = 0; i < 5; ++i) w[i] = (at >> 2) + i < s.lo ? s.head : (at >> 2) + i >= s.hi ? s.tail : v.w[i];
+  return make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                    __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
@@ -132,13 +159,27 @@ __device__ __forceinline__ void st_async_f4(uint32_t addr, uint32_t bar, float4 
                : "memory");
 }
 
-// The base of `count` (at most B) tokens t, t + step, ...: columns n .. n + 3 of this lane.
+// The base of `count` (at most B) tokens t, t + step, ...: columns n .. n + 3 of this lane, or (p.vec = 0)
+// the same four as in store_tokens.
 template <int B>
-__device__ __forceinline__ void load_tokens(const StreamParams& p, float4 (&b)[B], int t, int step, int count, int n) {
+__device__ __forceinline__ void load_tokens(const StreamParams& p, float4 (&b)[B], int t, int step, int count, int n, int lane) {
+#pragma unroll
+  for (int i = 0; i < B; ++i) b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.vec) {
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+      if (i < count && n < p.N) b[i] = *reinterpret_cast<const float4*>(p.base + int64_t(t + i * step) * p.N + n);
+    return;
+  }
+  n -= 3 * lane;
 #pragma unroll
   for (int i = 0; i < B; ++i) {
-    b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < count && n < p.N) b[i] = *reinterpret_cast<const float4*>(p.base + int64_t(t + i * step) * p.N + n);
+    if (i >= count) break;
+    const float* at = p.base + int64_t(t + i * step) * p.N + n;
+    if (n < p.N) b[i].x = at[0];
+    if (n + 32 < p.N) b[i].y = at[32];
+    if (n + 64 < p.N) b[i].z = at[64];
+    if (n + 96 < p.N) b[i].w = at[96];
   }
 }
 
@@ -149,12 +190,12 @@ template <int NW, int B>
 __device__ __forceinline__ void store_tokens(const StreamParams& p, float4 (&v)[B][NW], const float4 (&b)[B], int t, int step,
                                              int count, int n, int lane) {
   if (NW == 1) {
+    if (p.base) {
+#pragma unroll
+      for (int i = 0; i < B; ++i) v[i][0].x += b[i].x, v[i][0].y += b[i].y, v[i][0].z += b[i].z, v[i][0].w += b[i].w;
+    }
     if (p.vec) {  // N a multiple of 4, rows aligned: all four or none
       if (n >= p.N) return;
-      if (p.base) {
-#pragma unroll
-        for (int i = 0; i < B; ++i) v[i][0].x += b[i].x, v[i][0].y += b[i].y, v[i][0].z += b[i].z, v[i][0].w += b[i].w;
-      }
 #pragma unroll
       for (int i = 0; i < B; ++i) {
         if (i >= count) break;
@@ -176,9 +217,8 @@ __device__ __forceinline__ void store_tokens(const StreamParams& p, float4 (&v)[
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (n0 + 32 * j >= p.N) break;
-        const float s = p.base ? p.base[at + 32 * j] + o[j] : o[j];
-        if (p.out_bf16) static_cast<bf16*>(p.out)[at + 32 * j] = __float2bfloat16_rn(s);
-        else static_cast<float*>(p.out)[at + 32 * j] = s;
+        if (p.out_bf16) static_cast<bf16*>(p.out)[at + 32 * j] = __float2bfloat16_rn(o[j]);
+        else static_cast<float*>(p.out)[at + 32 * j] = o[j];
       }
     }
     return;
@@ -340,12 +380,35 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
       // scale words: each of the four warps writes them to its own lane quarter
       const int q0 = kb0 / 4, q1 = (kb1 - 1) / 4;
       const int cols = (p.bn + 31) / 32;
-      const Scales sx{p.sx, p.sx + int64_t(p.T) * p.KB};
+      const Scales sx = scales_of(p.sx, p.T * p.KB, p.sf_align);
       Scales sw[NW];
 #pragma unroll
-      for (int m = 0; m < NW; ++m) sw[m] = Scales{p.sw[m], p.sw[m] + int64_t((p.N + 127) / 128) * p.KB};
+      for (int m = 0; m < NW; ++m) sw[m] = scales_of(p.sw[m], (p.N + 127) / 128 * p.KB, p.sf_align);
       uint4 wa[NW], wb[8];
       auto load = [&](int r) {
+        if (p.sf_align == 1) {
+          ScaleWords a[NW], b[4];
+#pragma unroll
+          for (int m = 0; m < NW; ++m) a[m] = scale_words(sw[m], blockIdx.y, r, p.KB);
+#pragma unroll
+          for (int half = 0; half < 8; half += 4) {
+            if (half && cols <= half) break;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (half + c < cols) b[c] = scale_words(sx, min(tok0 + 32 * (half + c) + lane, p.T - 1), r, p.KB);
+            if (half == 0) {
+#pragma unroll
+              for (int m = 0; m < NW; ++m) wa[m] = scale_round(sw[m], blockIdx.y, r, p.KB, a[m]);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int t = tok0 + 32 * (half + c) + lane;
+              wb[half + c] = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
+              if (half + c < cols && t < p.T) wb[half + c] = scale_round(sx, t, r, p.KB, b[c]);
+            }
+          }
+          return;
+        }
 #pragma unroll
         for (int m = 0; m < NW; ++m) wa[m] = scale_round(sw[m], blockIdx.y, r, p.KB, p.sf_align);
 #pragma unroll
@@ -422,9 +485,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
     }
     constexpr int kBatch = 4;  // tokens per warp at a time: their loads and reductions overlap
     const int n = row0 + 4 * lane, first = tok0 + rank;
-    const bool read_base = NW == 1 && p.base && p.vec;
+    const bool read_base = NW == 1 && p.base;
     float4 base[kBatch];
-    if (read_base) load_tokens(p, base, first + (warp - 2) * splits, 8 * splits, (mine - (warp - 2) + 7) / 8, n);
+    if (read_base) load_tokens(p, base, first + (warp - 2) * splits, 8 * splits, (mine - (warp - 2) + 7) / 8, n, lane);
     // (an aborted CTA sends nothing: its owners' waits run out, and the status word says so)
     if (splits == 1) asm volatile("bar.sync 2, 256;" ::: "memory");
     else if (mine > 0) ok = named_bar_and(2, 256, mbar_wait_cluster(sums_full, 0, abort_flag, p.err));
@@ -433,7 +496,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
       const uint32_t src = (splits == 1 ? ring : sums) + (spread ? 4 : 16) * lane;
       for (int j0 = warp - 2; j0 < mine; j0 += 8 * kBatch) {
         const int count = (mine - j0 + 7) / 8;
-        if (read_base && j0 != warp - 2) load_tokens(p, base, first + j0 * splits, 8 * splits, count, n);
+        if (read_base && j0 != warp - 2) load_tokens(p, base, first + j0 * splits, 8 * splits, count, n, lane);
         float4 v[kBatch][NW];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
@@ -737,16 +800,30 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     // scale words of this CTA's tokens (4 columns) and of all 256 weight rows (8 columns)
     const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
     const int blocks = (p.N + 127) / 128;
-    const Scales sx{p.sx, p.sx + int64_t(p.T) * p.KB};
-    const Scales sw0{p.sw[0], p.sw[0] + int64_t(blocks) * p.KB};
-    const uint8_t* second = p.sw[kGated ? 1 : 0];
-    const Scales sw1{second, second + int64_t(blocks) * p.KB};
+    const Scales sx = scales_of(p.sx, p.T * p.KB, p.sf_align);
+    const Scales sw0 = scales_of(p.sw[0], blocks * p.KB, p.sf_align);
+    const Scales sw1 = kGated ? scales_of(p.sw[1], blocks * p.KB, p.sf_align) : sw0;
     uint4 a[4], u, v;
     auto load = [&](int tile, int r) {
       int mt, nt;
       pair_tile(p, tile, mt, nt);
       const int tok0 = mt * 256 + rank * 128 + lane;
       const int b0 = kGated ? nt : 2 * nt, b1 = kGated ? nt : 2 * nt + 1;
+      if (p.sf_align == 1) {
+        ScaleWords x[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = scale_words(sx, min(tok0 + 32 * c, p.T - 1), r, p.KB);
+        const ScaleWords y = scale_words(sw0, b0, r, p.KB), z = scale_words(sw1, min(b1, blocks - 1), r, p.KB);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          a[c] = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
+          if (tok0 + 32 * c < p.T) a[c] = scale_round(sx, tok0 + 32 * c, r, p.KB, x[c]);
+        }
+        u = scale_round(sw0, b0, r, p.KB, y);
+        v = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
+        if (b1 < blocks) v = scale_round(sw1, b1, r, p.KB, z);
+        return;
+      }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         a[c] = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
