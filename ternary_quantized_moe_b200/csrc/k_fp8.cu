@@ -67,6 +67,8 @@ struct StreamParams {
   int T, N, KB;
   int bn, stages, tmem_cols, sf_col, sfb_cols;
   int out_bf16, vec, sf_align;
+  int range, longer;  // K blocks of a CTA of the cluster, and how many have one more
+  uint32_t inverse;   // 2^16 / splits, rounded up: n inverse >> 16 is n / splits for n < 2^12
 };
 
 struct Bars {
@@ -254,10 +256,11 @@ __device__ __forceinline__ void store_tokens(const StreamParams& p, float4 (&v)[
   }
 }
 
-// NW = 1: out = base + W x.  NW = 2: h = silu(W0 x) (W1 x), to bf16 or codes and scales.  kLoose: rows of
-// outputs, bases and scales of any alignment (p.vec, p.sf_align); the kernel without is a shorter one, which
-// a launch of few us notices (2048 x 4096, 64 tokens: 6.9 us with, 6.8 without).
-template <int NW, bool kLoose>
+// NW = 1: out = base + W x.  NW = 2: h = silu(W0 x) (W1 x), to bf16 or codes and scales.  kSplit: K is split
+// over a cluster.  kLoose: rows of outputs, bases and scales of any alignment (p.vec, p.sf_align).  Both are
+// there because a launch of few us waits for its instructions, each of which runs once or twice (2048 x
+// 4096, 64 tokens: 6.9 us with the code for unaligned rows, 6.4 without).
+template <int NW, bool kSplit, bool kLoose>
 __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __grid_constant__ StreamParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   static_assert(sizeof(Bars) <= 1024, "shared memory");
@@ -269,13 +272,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
   const uint32_t acc_full = smem0 + offsetof(Bars, acc_full), done = smem0 + offsetof(Bars, done);
   const uint32_t sums_full = smem0 + offsetof(Bars, sums);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x, splits = gridDim.x;
+  const int rank = kSplit ? blockIdx.x : 0, splits = kSplit ? gridDim.x : 1;
   const int row0 = blockIdx.y * 128, tok0 = blockIdx.z * p.bn;
-  const int kb0 = int(int64_t(rank) * p.KB / splits), kb1 = int(int64_t(rank + 1) * p.KB / splits);
+  const int kb0 = rank * p.range + min(rank, p.longer), kb1 = kb0 + p.range + (rank < p.longer);
   const uint32_t block_bytes = NW * 16384 + p.bn * 128, stage_bytes = kStageBlocks<NW> * block_bytes;
   const int nt = min(p.bn, p.T - tok0);
+  const auto by_splits = [&](int n) { return kSplit ? int(uint32_t(n) * p.inverse >> 16) : n; };  // n / splits
   // this CTA's tokens (rank, rank + splits, ...) and what arrives for them: [token][sender][matrix][feature]
-  const int mine = rank < nt ? (nt - rank + splits - 1) / splits : 0;
+  const int mine = rank < nt ? by_splits(nt - rank + splits - 1) : 0;
   const uint32_t sums = ring + p.stages * stage_bytes;
 
   if (threadIdx.x == 0) {
@@ -292,14 +296,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
   tc_fence_before();
   __syncthreads();
   // the barriers of the cluster exist before anything is sent (awaited before the first store)
-  if (splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (kSplit) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = bars.tmem_slot;
   volatile int* abort_flag = &bars.abort_flag;
   pdl_trigger();
 
   // (every role that touches global memory waits for the predecessor grid itself, as late as it can)
-  bool joined = splits == 1;
+  bool joined = !kSplit;
   // the loops over K of warps 0 and 1 are run by the whole warp, with one lane (elect_one) issuing
   if (warp == 0) {
     RingPos at;
@@ -381,20 +385,21 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
     if (group == 0) {
       // scale words: each of the four warps writes them to its own lane quarter
       const int q0 = kb0 / 4, q1 = (kb1 - 1) / 4;
+      constexpr int kCols = kSplit ? 4 : 8;  // (a tile that splits K has up to 128 / NW tokens)
       const int cols = (p.bn + 31) / 32;
       const int align = kLoose ? p.sf_align : 4;
       const Scales sx = scales_of(p.sx, p.T * p.KB, align);
       Scales sw[NW];
 #pragma unroll
       for (int m = 0; m < NW; ++m) sw[m] = scales_of(p.sw[m], (p.N + 127) / 128 * p.KB, align);
-      uint4 wa[NW], wb[8];
+      uint4 wa[NW], wb[kCols];
       auto load = [&](int r) {
         if (kLoose && p.sf_align == 1) {
           ScaleWords a[NW], b[4];
 #pragma unroll
           for (int m = 0; m < NW; ++m) a[m] = scale_words(sw[m], blockIdx.y, r, p.KB);
 #pragma unroll
-          for (int half = 0; half < 8; half += 4) {
+          for (int half = 0; half < kCols; half += 4) {
             if (half && cols <= half) break;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
 #pragma unroll
         for (int m = 0; m < NW; ++m) wa[m] = scale_round(sw[m], blockIdx.y, r, p.KB, p.sf_align);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kCols; ++c) {
           const int t = tok0 + 32 * c + lane;
           wb[c] = make_uint4(kNoScale, kNoScale, kNoScale, kNoScale);
           if (c < cols && t < p.T) wb[c] = scale_round(sx, t, r, p.KB, p.sf_align);
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
       };
       load(q0 / 4);
       for (int r = q0 / 4; r <= q1 / 4 && ok; ++r) {
-#pragma unroll
+#pragma unroll 1
         for (int slot = 0; slot < kSfSlots; ++slot) {
           const int q = 4 * r + slot, i = q - q0;
           if (i < 0 || q > q1) continue;
@@ -439,8 +444,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
             tmem_st4(sf + 4 * m, w, w, w, w);
           }
           tmem_st4(sf + 4 * NW, word(wb[0], slot), word(wb[1], slot), word(wb[2], slot), word(wb[3], slot));
-          if (p.sfb_cols > 4)
-            tmem_st4(sf + 4 * NW + 4, word(wb[4], slot), word(wb[5], slot), word(wb[6], slot), word(wb[7], slot));
+          if (kCols > 4 && p.sfb_cols > 4)
+            tmem_st4(sf + 4 * NW + 4, word(wb[4 % kCols], slot), word(wb[5 % kCols], slot), word(wb[6 % kCols], slot), word(wb[7 % kCols], slot));
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&bars.sf_full[slot]);
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
       }
     }
     ok = named_bar_and(2, 256, ok && mbar_wait(acc_full, 0, abort_flag, p.err));
-    if (splits > 1) {
+    if (kSplit) {
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       joined = true;
     }
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
         for (int m = 0; m < NW; ++m) {
           float v[16];
           tmem_ld16(tmem + quarter + m * p.bn + c, v);
-          if (splits == 1) {
+          if (!kSplit) {
             // (over the ring: every load has been read by an MMA, and every MMA has finished)
             const uint32_t dst = ring + (c * NW + m) * 512 + feature;
 #pragma unroll
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int t = 4 * i + (lane >> 3), owner = (c + t) % splits, slot = (c + t) / splits;
+              const int t = 4 * i + (lane >> 3), slot = by_splits(c + t), owner = c + t - slot * splits;
               const float4 o = lds_f4(turn + t * 144 + (lane & 7) * 16);
               if (c + t < nt)
                 st_async_f4(map_cluster_rank(sums, owner) + ((slot * splits + rank) * NW + m) * 512 + (warp & 3) * 128 + (lane & 7) * 16,
@@ -492,11 +497,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
     float4 base[kBatch];
     if (read_base) load_tokens<kLoose>(p, base, first + (warp - 2) * splits, 8 * splits, (mine - (warp - 2) + 7) / 8, n, lane);
     // (an aborted CTA sends nothing: its owners' waits run out, and the status word says so)
-    if (splits == 1) asm volatile("bar.sync 2, 256;" ::: "memory");
+    if (!kSplit) asm volatile("bar.sync 2, 256;" ::: "memory");
     else if (mine > 0) ok = named_bar_and(2, 256, mbar_wait_cluster(sums_full, 0, abort_flag, p.err));
     if (ok) {
       const bool spread = kLoose && NW == 1 && !p.vec;
-      const uint32_t src = (splits == 1 ? ring : sums) + (spread ? 4 : 16) * lane;
+      const uint32_t src = (kSplit ? sums : ring) + (spread ? 4 : 16) * lane;
       for (int j0 = warp - 2; j0 < mine; j0 += 8 * kBatch) {
         const int count = (mine - j0 + 7) / 8;
         if (read_base && j0 != warp - 2) load_tokens<kLoose>(p, base, first + j0 * splits, 8 * splits, count, n, lane);
@@ -529,7 +534,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
   }
-  if (splits > 1) {
+  if (kSplit) {
     // an owner that gave up stays until nothing more can be sent to it; the others need not wait
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (*abort_flag) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -993,7 +998,7 @@ cudaError_t max_clusters(int n, int* count) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = n, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr, cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(count, fp8_stream_kernel<1, false>, &cfg);
+  return cudaOccupancyMaxActiveClusters(count, fp8_stream_kernel<1, true, false>, &cfg);
 }
 
 // Shape of a stream launch and what it is expected to take.
@@ -1048,6 +1053,7 @@ int launch_stream(const scion_fp8* L, const StreamPlan& plan, StreamParams& p, c
   p.w[0] = L->w[0], p.w[1] = L->w[NW - 1];
   p.bn = plan.bn;
   const int splits = plan.splits;
+  p.range = p.KB / splits, p.longer = p.KB % splits, p.inverse = 65536 / splits + 1;
   p.sfb_cols = p.bn > 128 ? 8 : 4;
   p.sf_col = NW * p.bn;
   p.tmem_cols = int(tmem_cols_pow2(p.sf_col + kSfSlots * (4 * NW + p.sfb_cols)));
@@ -1067,7 +1073,10 @@ int launch_stream(const scion_fp8* L, const StreamPlan& plan, StreamParams& p, c
   int st = make_tmap_codes(&p.x, x, T, L->desc.k, p.bn);
   if (st != SCION_OK) return st;
   const bool loose = p.sf_align == 1 || (NW == 1 && !p.vec);
-  return status(launch_pdl_cluster(loose ? fp8_stream_kernel<NW, true> : fp8_stream_kernel<NW, false>,
+  const auto kernel = splits > 1 ? loose ? fp8_stream_kernel<NW, true, true> : fp8_stream_kernel<NW, true, false>
+                      : loose    ? fp8_stream_kernel<NW, false, true>
+                                 : fp8_stream_kernel<NW, false, false>;
+  return status(launch_pdl_cluster(kernel,
                                    dim3(splits, plan.n_tiles, plan.t_tiles), dim3(kStreamThreads), dim3(splits, 1, 1), smem, s, p));
 }
 
@@ -1144,8 +1153,10 @@ extern "C" int scion_fp8_create(const scion_fp8_desc* D, void* stream, scion_fp8
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&L->sms, cudaDevAttrMultiProcessorCount, dev);
   // (a function attribute of the current device)
-  for (const auto f : {scion::fp8_stream_kernel<1, false>, scion::fp8_stream_kernel<2, false>, scion::fp8_stream_kernel<1, true>,
-                       scion::fp8_stream_kernel<2, true>})
+  for (const auto f : {scion::fp8_stream_kernel<1, false, false>, scion::fp8_stream_kernel<1, false, true>,
+                       scion::fp8_stream_kernel<1, true, false>, scion::fp8_stream_kernel<1, true, true>,
+                       scion::fp8_stream_kernel<2, false, false>, scion::fp8_stream_kernel<2, false, true>,
+                       scion::fp8_stream_kernel<2, true, false>, scion::fp8_stream_kernel<2, true, true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, scion::kSmem);
   for (const auto f : {scion::fp8_pair_kernel<scion::kPairBf16>, scion::fp8_pair_kernel<scion::kPairF32>,
                        scion::fp8_pair_kernel<scion::kPairBase>, scion::fp8_pair_kernel<scion::kPairLoose>,
