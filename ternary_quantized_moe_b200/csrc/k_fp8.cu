@@ -41,8 +41,8 @@ typedef __nv_bfloat16 bf16;
 // lane quarter, alternate 16-token chunks), warps 2..5 also the scale words.  The sums pass through
 // shared memory, so that a warp finishes one token at a time with four features per lane: one
 // reduction for a token's scale, 128 features in whole sectors.
-// Measured (replayed from a graph): 64 tokens, 16384 x 8192, 28.3 us (4.9 TB/s); 2048 x 4096 in clusters of
-// 4, 6.8 us, of which the K loop is two: start of the cluster, first copies, exchange and stores are the
+// Measured (replayed from a graph): 64 tokens, 16384 x 8192, 27.5 us (5.2 TB/s); 2048 x 4096 in clusters of
+// 4, 6.0 us, of which the K loop is two: start of the cluster, first copies, exchange and stores are the
 // rest.  A block of K of 128 takes 0.25 us (24 KB per SM: the rate of an SM's reads from L2).
 constexpr int kStreamThreads = 320;
 constexpr int kMaxStages = 8;
@@ -491,7 +491,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
         }
       }
     }
-    constexpr int kBatch = 4;  // tokens per warp at a time: their loads and reductions overlap
+    // Tokens per warp at a time: their loads and reductions overlap.  (64 tokens over a cluster leave a warp
+    // two, 6.2 us with a batch of four and 5.95 with two; 16384 x 8192 without a split 28.6 with two, 27.5.)
+    constexpr int kBatch = kSplit ? 2 : 4;
     const int n = row0 + 4 * lane, first = tok0 + rank;
     const bool read_base = NW == 1 && p.base;
     float4 base[kBatch];
@@ -510,6 +512,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) fp8_stream_kernel(const __g
         for (int i = 0; i < kBatch; ++i)
 #pragma unroll
           for (int m = 0; m < NW; ++m) v[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
         for (int r = 0; r < splits; ++r) {
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
@@ -1012,7 +1015,8 @@ struct StreamPlan {
 // 128 / nw tokens can split K over a cluster.  The estimate is a fit to launches of 8 to 128 tiles of
 // 32 to 128 tokens, K = 2048 to 8192 (within 10%): a start that grows with the tile's tokens (they
 // pass the epilogue one warp each), with the cluster and with the share of the SMs in use, and a time
-// per block of K, which the issuing of its MMAs bounds up to 128 tokens.
+// per block of K, which the issuing of its MMAs bounds up to 128 tokens.  Clusters that leave next to no SM
+// free start late: 1000 tokens, 1112 x 2048, take 8.6 us as 72 pairs of CTAs and 7.5 as 144 CTAs.
 StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
   StreamPlan best{};
   for (int most : {256, 128, 64}) {
@@ -1023,7 +1027,7 @@ StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
     const int64_t tiles = int64_t(p.n_tiles) * p.t_tiles;
     // (the sums of a wide tile would leave too little shared memory for the ring)
     for (p.splits = 1; p.splits <= (p.bn > 128 / nw ? 1 : std::min(8, KB)); ++p.splits) {
-      // all clusters at once: 16 tiles of 64 tokens, K = 4096, take 6.8 us in clusters of 4 and 12.4 in
+      // all clusters at once: 16 tiles of 64 tokens, K = 4096, took 6.8 us in clusters of 4 and 12.4 in
       // clusters of 8, of which 15 fit
       if (p.splits > 1 && L->clusters[p.splits] < tiles) break;
       const int range = (KB + p.splits - 1) / p.splits;
@@ -1031,9 +1035,9 @@ StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
       const double used = std::min(1.0, double(tiles * p.splits) / L->sms);
       const double wide = std::max(0, p.bn - 128 / nw);
       if (p.splits == 1)
-        p.us = waves * (2.0 + (nw == 1 ? 0.018 : 0.045) * p.bn + used + range * (nw == 1 ? 0.262 + 0.0015 * wide : 0.385 + 0.0012 * wide));
+        p.us = waves * ((nw == 1 ? 1.6 + 0.018 * p.bn : 2.0 + 0.045 * p.bn) + used + range * (nw == 1 ? 0.262 + 0.0015 * wide : 0.385 + 0.0012 * wide));
       else
-        p.us = (nw == 1 ? 2.3 + 0.024 * p.bn : 2.9 + 0.043 * p.bn) + 0.08 * p.splits + 1.8 * used + range * (nw == 1 ? 0.245 : 0.37);
+        p.us = (nw == 1 ? 1.6 + 0.018 * p.bn : 1.9 + 0.034 * p.bn) + 0.08 * p.splits + 1.8 * used + (used > 0.9) + range * (nw == 1 ? 0.245 : 0.37);
       if (!best.bn || p.us < best.us) best = p;
     }
   }
@@ -1045,7 +1049,7 @@ StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
 double pair_us(const scion_fp8* L, int nw, int T, int N, int KB, bool base) {
   const int64_t tiles = int64_t((T + 255) / 256) * (nw == 1 ? (N + 255) / 256 : (N + 127) / 128);
   const int pairs = std::max(1, L->sms / 2);
-  return (nw == 1 ? 3.1 : 3.9) + double((tiles + pairs - 1) / pairs) * (1.0 + 0.33 * KB + (base ? 3.5 : 0.0));
+  return (nw == 1 ? 3.7 : 4.3) + double((tiles + pairs - 1) / pairs) * (1.0 + 0.33 * KB + (base ? 3.5 : 0.0));
 }
 
 template <int NW>
@@ -1080,18 +1084,17 @@ int launch_stream(const scion_fp8* L, const StreamPlan& plan, StreamParams& p, c
                                    dim3(splits, plan.n_tiles, plan.t_tiles), dim3(kStreamThreads), dim3(splits, 1, 1), smem, s, p));
 }
 
-// Up to 8 tokens, and up to 16 or 32 with few weights, run on mma.sync (k_fp8_rows.cu): it starts sooner,
-// but reads the tokens again for every 16 weight rows and its products are slower (about 50 cycles per
-// step of 8 tokens x 16 rows x 32 columns).  n x k, us against the stream kernel: 2048 x 4096, 1 token 2.8
-// against 4.9, 16 tokens 3.6 against 5.3; 16 tokens, 4096 x 4096 5.4 against 7.0, 8192 x 8192 22.6 against
-// 15.4; 32 tokens, 2048 x 2048 3.7 against 5.4, 4096 x 2048 5.4 against 5.9, 2048 x 4096 5.6 against 6.1,
-// 1024 x 8192 9.5 against 6.7, 4096 x 4096 8.4 against 7.2.  Gated, 16 tokens, 2 x 2048 x 2048 6.4 against
-// 6.7, 2 x 2048 x 5456 12.2 against 8.0; 32 tokens, 2 x 512 x 2048 6.2 against 6.0.
+// Few tokens and few weights run on mma.sync (k_fp8_rows.cu): it starts sooner, but reads the tokens again
+// for every 16 weight rows, and its products are slower (about 50 cycles per step of 8 tokens x 16 rows x 32
+// columns).  n x k, us against the stream kernel, 8 tokens: 2048 x 2048 2.6 against 4.2, 8192 x 8192 14.1
+// against 14.7; 16 tokens: 4096 x 4096 5.4, 5.9; 8192 x 2048 5.8, 5.7; 8192 x 8192 22.1, 15.1; 32 tokens:
+// 2048 x 2048 3.7, 4.7; 4096 x 2048 5.3, 5.4; 1024 x 4096 5.5, 4.8.  Gated, 8 tokens: 2 x 4096 x 2048 5.2, 5.8;
+// 2 x 1024 x 8192 7.6, 7.0; 2 x 8192 x 2048 9.0, 7.1; 16 tokens: 2 x 1024 x 2048 4.3, 4.8; 2 x 2048 x 2048 6.6,
+// 5.2; 2 x 4096 x 512 4.9, 4.6.
 bool use_rows(const Call& c) {
   const int64_t weights = int64_t(c.N) * c.K;
-  if (c.T <= 8) return true;
-  if (c.w[1]) return c.T <= 16 && weights <= 5 << 20;
-  return c.T <= 16 ? weights <= 24 << 20 : c.T <= 32 && c.K <= 4096 && weights <= 8 << 20;
+  if (c.w[1]) return c.T <= 8 ? c.K <= 4096 && weights <= 8 << 20 : c.T <= 16 && c.N <= 2048 && weights <= 2 << 20;
+  return c.T <= 8 || (c.T <= 16 ? weights <= 16 << 20 : c.T <= 32 && c.K <= 2048 && weights <= 4 << 20);
 }
 
 template <int EPI>

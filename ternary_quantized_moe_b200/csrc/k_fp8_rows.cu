@@ -11,7 +11,7 @@
 // A gated layer that writes 8 bits needs the largest |h| of 128 features: the eight CTAs of a cluster
 // hold them and exchange one magnitude per token.
 // Measured (replayed from a graph, one token): 4096 x 2048 2.5 us, 16384 x 8192 25.5 us (5.3 TB/s), gated
-// 2 x 512 x 2048 3.1 us; 8 tokens, gated 2 x 8192 x 4096 15.5 us (4.3 TB/s).
+// 2 x 512 x 2048 3.1 us; 8 tokens, gated 2 x 2048 x 4096 5.8 us.
 #include "fp8_common.cuh"
 #include "scion_internal.cuh"
 
@@ -222,17 +222,17 @@ cudaError_t launch(const Call& c, cudaStream_t s) {
 template <int NW, bool G>
 cudaError_t launch_tokens(const Call& c, cudaStream_t s) {
   const int ctas = (c.N + 15) / 16;
-  const bool few = ctas <= c.sms, longer = c.KB > 2 * kRowsWarps;
   if constexpr (NW == 1) {
+    const bool few = ctas <= c.sms, longer = c.KB > 2 * kRowsWarps;
     if (c.T > 16) return few ? launch<1, 4, 1, G, 1>(c, s) : launch<1, 4, 1, G, 2>(c, s);
     if (c.T > 8) return few ? launch<1, 2, 2, G, 1>(c, s) : launch<1, 2, 1, G, 2>(c, s);
     if (few && longer) return launch<1, 1, 4, G, 1>(c, s);
     return ctas <= 2 * c.sms ? launch<1, 1, 2, G, 2>(c, s) : launch<1, 1, 2, G, 4>(c, s);
   } else {
     // With one CTA per SM, clusters of 8 CTAs fill little more than three quarters of the SMs.  16 tokens,
-    // 2 x 1024 x 4096 (64 CTAs): one per SM 6.2, two (which spills 136 bytes) 7.8; 2 x 2048 x 2048 (128) 7.8, 6.5.
+    // 64 CTAs (2 x 1024 x 4096): one per SM 6.2, two (which spills 136 bytes) 7.8; 128 (2 x 2048 x 2048) 7.8, 6.5.
     if (c.T > 8) return ctas <= c.sms * 3 / 4 ? launch<2, 2, 1, G, 1>(c, s) : launch<2, 2, 1, G, 2>(c, s);
-    return longer && !few ? launch<2, 1, 2, G, 2>(c, s) : launch<2, 1, 1, G, 2>(c, s);
+    return launch<2, 1, 1, G, 2>(c, s);
   }
 }
 
