@@ -125,6 +125,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, PerSm) fp8_rows_kernel(const 
   __shared__ uint32_t amax[8][8 * NT];                // [CTA of the cluster][token]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int row0 = blockIdx.x * 16;
+  // (shared memory of another CTA may be used once all of the cluster run: awaited before the first store)
+  if (G) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   Lane<NW, NT> l;
 #pragma unroll
   for (int m = 0; m < NW; ++m) {
@@ -153,6 +155,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, PerSm) fp8_rows_kernel(const 
 #pragma unroll
       for (int i = 0; i < 4; ++i) part[warp][m][8 * t + 2 * c + (i & 1)][g + 8 * (i >> 1)] = acc[m][t][i];
   __syncthreads();
+  if (G) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   // thread: row threadIdx % 16 of tokens threadIdx / 16, 16 further, ... (a half warp per token)
   constexpr int kPasses = (NT + 1) / 2;
   const int r = threadIdx.x & 15, tok0 = threadIdx.x >> 4, n = row0 + r;
