@@ -364,9 +364,10 @@ int scion_fp8_quantize_device(int src_type, const void* src, int64_t rows, int c
  * with one scale per 128 columns, both or neither; at least one of resid_out, y_bf16 and y_codes
  * is given.  r and the statistic are fp32, and the norm is taken of r before it is rounded to
  * resid_type; the 8-bit output is quantized from the fp32 y.  A row that holds an infinity or a
- * NaN, or whose sum of squares leaves the fp32 range, gives NaN in all of its y; y is formed as
- * (r * weight) times the statistic, and r * weight has to stay in the fp32 range too.  A row's
- * result does not depend on the rows beside it.
+ * NaN, or whose sum of squares is above the fp32 range, gives NaN in all of its y, and so does a row
+ * of zeros with eps = 0 (0 / 0); rows of any smaller magnitude are normed like others, whatever eps
+ * is.  y is formed as (r * weight) times the statistic, and r * weight has to stay in the fp32 range
+ * too.  A row's result does not depend on the rows beside it.
  * d a multiple of 16, d <= 32768; T >= 0 (T = 0 is a no-op); eps >= 0 and finite.  x, resid,
  * resid_out, weight, y_bf16 and y_codes 16-byte aligned; no output may overlap another argument
  * except as said.  EINVAL, ECUDA. */

@@ -55,13 +55,36 @@ struct NormParams {
 // chunks t, t + lanes, ..., so that the row stays in registers between the statistic and the output.
 // y = (r w) rms: the products r w and their largest magnitude per group do not wait for the statistic,
 // and (rounding is monotonic) max |y| = max |r w| rms to the last bit.
-template <typename X, typename R, int CPT, bool kBlock>
+// Squares below 2^-126 lose bits, which matters only where neither eps nor the rest of the sum is far
+// above them: with eps < kTiny (kSmallEps) the squares of r kLift are summed beside, and a row whose sum
+// is below kTiny (|r| < 2^-30, so that (r kLift)^2 sums to less than 2^120; the least fp32 gives 2^-118)
+// takes its statistic from those.  (A variant of its own: as a branch on eps it kept loads apart, 16384 x
+// 4096 bf16 without a residual in 55 us, 48 without it.)
+constexpr float kTiny = 0x1p-60f, kLift = 0x1p90f;
+
+// Sum over the row's threads, the same in all of them; `part`: 32 floats of shared memory per sum.
+template <bool kBlock>
+__device__ __forceinline__ float row_sum(float v, int t, int lanes, float* part) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (kBlock) {
+    const int lane = t & 31;
+    if (lane == 0) part[t >> 5] = v;
+    __syncthreads();
+    v = lane < (lanes >> 5) ? part[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
+  return v;
+}
+
+template <typename X, typename R, int CPT, bool kBlock, bool kSmallEps>
 __device__ __forceinline__ void norm_row(const NormParams& p, int64_t r, int t, int lanes, float* part) {
   const int64_t row = r * p.d;
   const int chunks = p.d >> 3;
   float v[CPT][8];
   uint32_t m[CPT];
-  float ss = 0.f;
+  float ss = 0.f, lifted = 0.f;
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = t + i * lanes;
@@ -82,23 +105,30 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t r, int t, 
     }
     float wf[8];
     unpack_bf16x8(w, wf);
+    if (kSmallEps) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) lifted = fmaf(v[i][j] * kLift, v[i][j] * kLift, lifted);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss), v[i][j] *= wf[j];
     if (p.codes) m[i] = half_warp_max(mag8(v[i]));
   }
   if (!p.y && !p.codes) return;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (kBlock) {
-    const int lane = t & 31;
-    if (lane == 0) part[t >> 5] = ss;
-    __syncthreads();
-    ss = lane < (lanes >> 5) ? part[lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  }
+  ss = row_sum<kBlock>(ss, t, lanes, part);
   // an infinite sum would turn the row's finite elements into zeros: the whole row is NaN instead
-  const float rms = ss < INFINITY ? rsqrtf(ss / float(p.d) + p.eps) : NAN;
+  float rms = ss < INFINITY ? rsqrtf(ss / float(p.d) + p.eps) : NAN;
+  if (kSmallEps) {
+    lifted = row_sum<kBlock>(lifted, t, lanes, part + 32);
+    if (ss < kTiny) {  // (a row of zeros without eps: 0 / 0 in every element)
+      rms = rsqrtf(lifted / float(p.d) + p.eps * kLift * kLift);
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= kLift;
+        if (p.codes) m[i] = mag(__uint_as_float(m[i]) * kLift);
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = t + i * lanes;
@@ -116,36 +146,40 @@ __device__ __forceinline__ void norm_row(const NormParams& p, int64_t r, int t, 
 }
 
 // A CTA per row.
-template <typename X, typename R, int CPT>
+template <typename X, typename R, int CPT, bool kSmallEps>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
-  __shared__ float part[32];
+  __shared__ float part[64];
   pdl_trigger();
   pdl_wait();
-  norm_row<X, R, CPT, true>(p, blockIdx.x, threadIdx.x, blockDim.x, part);
+  norm_row<X, R, CPT, true, kSmallEps>(p, blockIdx.x, threadIdx.x, blockDim.x, part);
 }
 
 // A warp per row, eight rows per CTA: no barrier.
-template <typename X, typename R, int CPT>
+template <typename X, typename R, int CPT, bool kSmallEps>
 __global__ void __launch_bounds__(256) rmsnorm_warp_kernel(const NormParams p, int T) {
   pdl_trigger();
   pdl_wait();
   const int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (r < T) norm_row<X, R, CPT, false>(p, r, threadIdx.x & 31, 32, nullptr);
+  if (r < T) norm_row<X, R, CPT, false, kSmallEps>(p, r, threadIdx.x & 31, 32, nullptr);
 }
 
-template <typename X, typename R>
+template <typename X, typename R, bool kSmallEps>
 cudaError_t launch_norm(const NormParams& p, int T, cudaStream_t s) {
   const int chunks = p.d >> 3;
   // 16384 rows of 128 fp32: 7 us with a warp per row, 17 with a CTA
-  if (chunks <= 64) return launch_pdl(rmsnorm_warp_kernel<X, R, 2>, dim3(unsigned((int64_t(T) + 7) / 8)), dim3(256), 0, s, p, T);
+  if (chunks <= 64) return launch_pdl(rmsnorm_warp_kernel<X, R, 2, kSmallEps>, dim3(unsigned((int64_t(T) + 7) / 8)), dim3(256), 0, s, p, T);
   // One chunk per thread is the quickest for few rows (1 x 4096 fp32: 2.2 us, 2.6 with two) and as good
   // for many, except where a thread would read 16 bytes in all (16384 x 4096 bf16 without a residual: 66
   // us, 54 with two) or the CTA have 1024 threads (8192 x 8192 bf16: 83 us, 80).
   const int cpt = chunks > 2048 ? 4 : chunks > 512 || (chunks > 256 && sizeof(X) == 2 && !p.resid) ? 2 : 1;
   const int nt = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
-  if (cpt == 1) return launch_pdl(rmsnorm_kernel<X, R, 1>, dim3(T), dim3(nt), 0, s, p);
-  if (cpt == 2) return launch_pdl(rmsnorm_kernel<X, R, 2>, dim3(T), dim3(nt), 0, s, p);
-  return launch_pdl(rmsnorm_kernel<X, R, 4>, dim3(T), dim3(nt), 0, s, p);
+  if (cpt == 1) return launch_pdl(rmsnorm_kernel<X, R, 1, kSmallEps>, dim3(T), dim3(nt), 0, s, p);
+  if (cpt == 2) return launch_pdl(rmsnorm_kernel<X, R, 2, kSmallEps>, dim3(T), dim3(nt), 0, s, p);
+  return launch_pdl(rmsnorm_kernel<X, R, 4, kSmallEps>, dim3(T), dim3(nt), 0, s, p);
+}
+template <typename X, typename R>
+cudaError_t launch_norm(const NormParams& p, int T, cudaStream_t s) {
+  return p.eps < kTiny ? launch_norm<X, R, true>(p, T, s) : launch_norm<X, R, false>(p, T, s);
 }
 
 // ------------------------------------------------------------------ quantizers
