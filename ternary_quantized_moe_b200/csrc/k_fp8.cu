@@ -1067,9 +1067,12 @@ int launch_stream(const scion_fp8* L, const StreamPlan& plan, StreamParams& p, c
   const uint32_t share = 228 * 1024 / 512 * p.tmem_cols - 1024;
   const uint32_t stage = kStageBlocks<NW> * (NW * 16384 + p.bn * 128);
   const uint32_t fixed = 2048 + (splits > 1 ? (p.bn + splits - 1) / splits * splits * NW * 512 : 0);
-  // two CTAs per SM where there are more than SMs
+  // Two CTAs per SM where there are more than SMs, unless that leaves one stage to each (tiles of 96 to 208
+  // tokens of a plain layer), whose copies would wait for the MMAs and they for them: 20480 x 8192, 96 tokens
+  // 53.2 us, 46.7 with one CTA and three stages (the pair kernel 50.9); 128 tokens 54.7, 49.3 (51.6).
   const bool crowded = int64_t(plan.n_tiles) * plan.t_tiles * splits > L->sms;
-  const uint32_t budget = crowded ? std::max<uint32_t>(share, 113 * 1024) : kSmem;
+  const uint32_t half = std::max<uint32_t>(share, 113 * 1024);
+  const uint32_t budget = crowded && half >= fixed + 2 * stage ? half : kSmem;
   const int range = (p.KB + splits - 1) / splits;  // K blocks of a CTA, at most
   p.stages = std::max(1, std::min({kMaxStages, int((budget - fixed) / stage), (range + kStageBlocks<NW> - 1) / kStageBlocks<NW>}));
   const uint32_t smem = std::max({fixed + p.stages * stage, uint32_t(2048 + NW * p.bn * 512), share});
