@@ -483,10 +483,13 @@ def _bind():
         if not os.path.exists(os.path.join(_PKG, "_binding.so")):
             raise ImportError("_binding.so is not built (run __graft_entry__.build() or "
                               "python -m ternary_quantized_moe_b200.build); there is no fallback path")
-        import torch  # noqa: F401  (its libraries are the extension's)
+        import torch  # (its libraries are the extension's)
 
         from . import _binding
 
+        if _binding.torch_version != torch.__version__:  # (it reads torch's objects by their C++ layout)
+            raise ImportError("_binding.so was built with torch %s, this is torch %s: build it again"
+                              % (_binding.torch_version, torch.__version__))
         _binding.init(*(C.cast(getattr(lib, n), C.c_void_p).value for n in (
             "scion_rmsnorm_forward", "scion_fp8_quantize_device", "scion_fp8_forward", "scion_fp8_gated_forward")))
         _ext = _binding

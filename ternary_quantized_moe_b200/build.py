@@ -13,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -22,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libscion.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_KEY = os.path.join(BUILD, "binding.key")  # what the extension was built with
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
@@ -53,22 +55,43 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_binding() -> None:
-    src = os.path.join(CSRC, "binding.cpp")
-    if not _stale(BINDING, [src, os.path.join(ROOT, "include", "scion.h")]):
-        return
+def _binding_command(out: str) -> list:
+    """The compiler's command for the extension: torch's headers, libraries and C++ ABI, this Python's headers."""
     import torch
     from torch.utils.cpp_extension import include_paths
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     inc = include_paths() + [cuda, sysconfig.get_paths()["include"]]
+    return ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, '-DSCION_TORCH="%s"' % torch.__version__]
+            + ["-isystem" + i for i in inc]
+            + [os.path.join(CSRC, "binding.cpp"), "-o", out, "-L" + lib, "-Wl,-rpath," + lib,
+               "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"])
+
+
+def _binding_key() -> str:
+    """What the extension depends on beside its sources (the command holds torch's version and paths)."""
+    return "\n".join([sys.implementation.cache_tag] + _binding_command("_binding.so")) + "\n"
+
+
+def _binding_stale() -> bool:
+    if _stale(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "scion.h")]):
+        return True
+    if not os.path.exists(BINDING_KEY):
+        return True
+    with open(BINDING_KEY) as f:
+        return f.read() != _binding_key()
+
+
+def _build_binding() -> None:
+    if not _binding_stale():
+        return
     tmp = BINDING + ".tmp%d" % os.getpid()
-    subprocess.check_call([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-                           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
-                          + ["-isystem" + i for i in inc] + [src, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib,
-                             "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"])
+    subprocess.check_call(_binding_command(tmp))
     os.replace(tmp, BINDING)
+    with open(BINDING_KEY, "w") as f:
+        f.write(_binding_key())
 
 
 def build(verbose: bool = False) -> str:
