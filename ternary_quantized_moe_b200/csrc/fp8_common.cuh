@@ -48,9 +48,6 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
 __device__ __forceinline__ float scale_inverse(uint32_t b) {
   return __uint_as_float(b == 255u ? 0x7fffffffu : (254u - b) << 23);
 }
-__device__ __forceinline__ float scale_value(uint32_t b) {
-  return b == 255u ? __uint_as_float(0x7fffffffu) : b ? __uint_as_float(b << 23) : __uint_as_float(0x00400000u);
-}
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
