@@ -12,6 +12,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "fp8_common.cuh"
 #include "scion_internal.cuh"
@@ -303,13 +304,24 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const S* __restric
   if (threadIdx.x == 0) scales[blockIdx.x] = uint8_t(b);
 }
 
+// SMs of the current device.
+int sm_count() {
+  static std::atomic<int> known[16];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 16 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 148;
+  if (dev < 16) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 template <typename S>
 cudaError_t launch_quantize(const S* src, int64_t rows, int cols, int block_rows, uint8_t* codes, uint8_t* scales,
                             cudaStream_t s) {
   const int groups = (cols + 127) / 128;
   if (block_rows == 1) {
     // 64 groups per CTA where that leaves two CTAs for every SM; the grid stays within 2^31 - 1
-    int64_t per = std::max<int64_t>(1, std::min<int64_t>(64 / groups, rows / 296));
+    int64_t per = std::max<int64_t>(1, std::min<int64_t>(64 / groups, rows / (2 * sm_count())));
     per = std::max(per, rows >> 30);
     return launch_pdl(quantize_rows_kernel<S>, dim3(unsigned((rows + per - 1) / per)), dim3(256), 0, s, src, rows, cols,
                       groups, int(per), codes, scales);
