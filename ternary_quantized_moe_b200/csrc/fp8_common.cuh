@@ -24,6 +24,7 @@ struct Call {
   uint8_t* scales;
   int T, N, K, KB;  // KB = ceil(K / 128)
   int out_bf16, sms;
+  int clusters8;  // clusters of 8 CTAs that run at once with one CTA per SM
 };
 
 // k_fp8_rows.cu: up to 32 tokens

@@ -1087,17 +1087,32 @@ int launch_stream(const scion_fp8* L, const StreamPlan& plan, StreamParams& p, c
                                    dim3(splits, plan.n_tiles, plan.t_tiles), dim3(kStreamThreads), dim3(splits, 1, 1), smem, s, p));
 }
 
-// Few tokens and few weights run on mma.sync (k_fp8_rows.cu): it starts sooner, but reads the tokens again
-// for every 16 weight rows, and its products are slower (about 50 cycles per step of 8 tokens x 16 rows x 32
-// columns).  n x k, us against the stream kernel, 8 tokens: 2048 x 2048 2.6 against 4.2, 8192 x 8192 14.1
-// against 14.7; 16 tokens: 4096 x 4096 5.4, 5.9; 8192 x 2048 5.8, 5.7; 8192 x 8192 22.1, 15.1; 32 tokens:
-// 2048 x 2048 3.7, 4.7; 4096 x 2048 5.3, 5.4; 1024 x 4096 5.5, 4.8.  Gated, 8 tokens: 2 x 4096 x 2048 5.2, 5.8;
-// 2 x 1024 x 8192 7.6, 7.0; 2 x 8192 x 2048 9.0, 7.1; 16 tokens: 2 x 1024 x 2048 4.3, 4.8; 2 x 2048 x 2048 6.6,
-// 5.2; 2 x 4096 x 512 4.9, 4.6.
+// Few tokens run on mma.sync (k_fp8_rows.cu) as long as the weights are few: it starts sooner, but reads the
+// tokens again for every 16 weight rows, its products are slower (about 50 cycles per step of 8 tokens x 16
+// rows x 32 columns), and a second round of its CTAs costs more than the streaming kernel's one.  The bounds
+// follow rounds of CTAs (16 weight rows on each of the SMs), from both kernels measured at K = 128 to 8192, n =
+// 256 to 65536, 1 to 32 tokens: the kernel taken was at most 11% behind the other.  n x k, us, rows against
+// stream.  8 tokens: 4096 x 4096 3.9, 5.8; 16384 x 512 3.6, 3.9; 16384 x 8192 27.5, 28.0; 32768 x 512 6.0, 4.4;
+// 65536 x 512 10.6, 12.6 (two rounds of the streaming kernel).  16 tokens: 4096 x 4096 5.3, 5.9; 8192 x 1024
+// 4.0, 4.5; 16384 x 512 6.0, 3.9; 8192 x 4096 10.1, 7.7.  32 tokens: 4096 x 1024 3.8, 4.6; 2048 x 2048 3.7,
+// 4.8; 8192 x 512 5.1, 3.7; 2048 x 4096 5.7, 5.4.  Gated to 8 bits, 8 tokens: 4096 x 2048 5.1, 5.8; 4096 x 4096
+// 6.6, 7.3; 4736 x 1024 5.4, 4.8; 1024 x 8192 7.1, 6.8; to bf16: 8192 x 2048 6.4, 6.9; 8192 x 2560 8.7, 8.0.
+// Gated, 16 tokens, to 8 bits: 1920 x 2560 5.2, 5.6; 1024 x 3584 6.0, 5.6; 2368 x 512 4.2, 4.3; 2048 x 1024
+// 4.8, 4.7; to bf16: 2368 x 2560 4.4, 5.6; 256 x 3584 5.1, 4.9; 4736 x 1024 4.6, 4.9; 4096 x 2048 6.5, 5.8.
 bool use_rows(const Call& c) {
-  const int64_t weights = int64_t(c.N) * c.K;
-  if (c.w[1]) return c.T <= 8 ? c.K <= 4096 && weights <= 8 << 20 : c.T <= 16 && c.N <= 2048 && weights <= 2 << 20;
-  return c.T <= 8 || (c.T <= 16 ? weights <= 16 << 20 : c.T <= 32 && c.K <= 2048 && weights <= 4 << 20);
+  const int64_t round = 16 * int64_t(c.sms), weights = int64_t(c.N) * c.K;
+  if (!c.w[1]) {
+    if (c.T <= 8) return c.N <= 8 * round || c.N > 16 * round;
+    if (c.T <= 16) return c.N <= 4 * round && weights <= 20 << 20;
+    return c.T <= 32 && c.N <= 2 * round && c.K <= 2048 && weights <= 5 << 20;
+  }
+  if (c.T <= 8) {
+    if (c.codes) return c.N <= 4096 && c.K <= 4096;  // (clusters of 8 CTAs, two to an SM)
+    return c.N <= 2 * round ? c.K <= 4096 : c.N <= 4 * round && c.K <= 2048;
+  }
+  if (c.T > 16) return false;
+  if (c.codes) return c.N <= 128 * c.clusters8 ? c.K <= 2560 : c.N <= round && c.K <= 768;
+  return c.N <= round ? c.K <= 3584 : c.N <= 2 * round && c.K <= 1024;
 }
 
 template <int EPI>
@@ -1120,7 +1135,7 @@ Call call(const scion_fp8* L, const uint8_t* x, const uint8_t* sx, int T) {
   Call c{};
   c.x = x, c.sx = sx;
   c.w[0] = L->desc.w_codes, c.sw[0] = L->desc.w_scales, c.w[1] = L->desc.up_codes, c.sw[1] = L->desc.up_scales;
-  c.T = T, c.N = L->desc.n, c.K = L->desc.k, c.KB = (c.K + 127) / 128, c.sms = L->sms;
+  c.T = T, c.N = L->desc.n, c.K = L->desc.k, c.KB = (c.K + 127) / 128, c.sms = L->sms, c.clusters8 = L->clusters[8];
   return c;
 }
 

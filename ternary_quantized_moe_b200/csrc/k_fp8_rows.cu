@@ -216,12 +216,15 @@ cudaError_t launch(const Call& c, cudaStream_t s) {
   return launch_pdl(fp8_rows_kernel<NW, NT, U, G, PerSm>, dim3(ctas), block, 0, s, c);
 }
 
-// Registers against CTAs.  Where every SM has one CTA at most, its warps take the registers to keep a
-// whole row's blocks in flight; where there are many, more CTAs per SM keep more loads in flight than
-// deeper ones.  One token, n x k (us): 2048 x 4096 (128 CTAs) U = 4 with registers for one CTA per SM 2.9,
-// for two 3.9; 4096 x 4096 (256) 4.8, 4.0, U = 2 3.7; 8192 x 8192 (512) U = 4 for two 15.9, U = 2 for four
-// 13.9.  16 tokens: 2048 x 4096 U = 2 for one 3.7, for two 4.6; 4096 x 4096 6.6, U = 1 5.4.  32 tokens (U =
-// 1): 2048 x 2048 for one 3.7, for two 5.1; 4096 x 2048 6.6, 5.4.
+// Registers against CTAs.  Where every SM has one CTA at most, its warps take the registers to keep a whole
+// row's blocks in flight; where there are many, more CTAs per SM keep more loads in flight than deeper ones.
+// One token, n x k (us): 2048 x 4096 (128 CTAs) U = 4 with registers for one CTA per SM 2.9, for two 3.9; 4096
+// x 4096 (256) 4.8, 4.0, U = 2 3.7; 8192 x 8192 (512) U = 4 for two 15.9, U = 2 for four 13.9.  16 tokens: 2048
+// x 4096 U = 2 for one 3.7, for two 4.6; 4096 x 4096 6.6, U = 1 5.4.  32 tokens (U = 1): 2048 x 2048 for one
+// 3.7, for two 5.1; 2400 x 1024 4.1, 3.6; 4096 x 512 3.8, 3.0 (24 tokens).  Gated, 16 tokens: registers for two
+// CTAs per SM spill (136 bytes), so that even two rounds of one are quicker, 2 x 2048 x 1024 to bf16 2.6
+// against 4.1; to 8 bits 2 x 1792 x 1024 3.4, 4.8, but 2 x 2048 x 512, 16 clusters of which 15 run at once with
+// one CTA per SM, 5.0, 3.9.
 template <int NW, bool G>
 cudaError_t launch_tokens(const Call& c, cudaStream_t s) {
   const int ctas = (c.N + 15) / 16;
@@ -232,9 +235,11 @@ cudaError_t launch_tokens(const Call& c, cudaStream_t s) {
     if (few && longer) return launch<1, 1, 4, G, 1>(c, s);
     return ctas <= 2 * c.sms ? launch<1, 1, 2, G, 2>(c, s) : launch<1, 1, 2, G, 4>(c, s);
   } else {
-    // With one CTA per SM, clusters of 8 CTAs fill little more than three quarters of the SMs.  16 tokens,
-    // 64 CTAs (2 x 1024 x 4096): one per SM 6.2, two (which spills 136 bytes) 7.8; 128 (2 x 2048 x 2048) 7.8, 6.5.
-    if (c.T > 8) return ctas <= c.sms * 3 / 4 ? launch<2, 2, 1, G, 1>(c, s) : launch<2, 2, 1, G, 2>(c, s);
+    if (c.T > 8) {
+      if constexpr (G)
+        if ((ctas + 7) / 8 > c.clusters8) return launch<2, 2, 1, G, 2>(c, s);
+      return launch<2, 2, 1, G, 1>(c, s);
+    }
     return launch<2, 1, 1, G, 2>(c, s);
   }
 }
