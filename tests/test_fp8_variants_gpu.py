@@ -99,3 +99,35 @@ def test_rows_kernel_gated(kernel, T, K, F):
 def test_rows_kernel_gated_more_clusters_than_run_at_once(T, K, F):
     """19 clusters of eight CTAs: 148 SMs hold 18 at most."""
     check_gated("fp8_rows_kernel<2, 2, 1, true, 2>", T, K, F, ("true",))
+
+
+# (kernel, T, K, N, base): scale rows and outputs of any alignment in the "true" of the third place
+PLAIN = [("fp8_stream_kernel<1, true, false>", 64, 4096, 2048, False), ("fp8_stream_kernel<1, true, false>", 64, 8192, 512, True),
+         ("fp8_stream_kernel<1, true, true>", 64, 4112, 2052, False), ("fp8_stream_kernel<1, true, true>", 64, 2048, 2049, True),
+         ("fp8_stream_kernel<1, false, false>", 500, 1024, 2048, False),
+         ("fp8_stream_kernel<1, false, false>", 600, 512, 2048, True),
+         ("fp8_stream_kernel<1, false, true>", 500, 1040, 2047, True), ("fp8_stream_kernel<1, false, true>", 500, 1040, 2048, False),
+         ("fp8_pair_kernel<0>", 2600, 1040, 2304, False), ("fp8_pair_kernel<1>", 2600, 1040, 2304, False),
+         ("fp8_pair_kernel<2>", 2600, 1040, 2304, True), ("fp8_pair_kernel<5>", 2600, 1040, 2303, False),
+         ("fp8_pair_kernel<5>", 2600, 1040, 2303, True)]
+
+
+@pytest.mark.parametrize("kernel,T,K,N,with_base", PLAIN)
+def test_stream_and_pair_kernels(kernel, T, K, N, with_base):
+    c = Case(T, K, N)
+    base = torch.from_numpy(c.base).to("cuda") if with_base else None
+    for out_type in (F32, BF16):
+        c.check(c.run(out_type, base), c.base if with_base else None)
+    out = torch.empty((T, N), dtype=BF16 if kernel.endswith("<0>") else F32, device="cuda")
+    check_launched(lambda: tq.scion_fp8_forward(c.dx, c.dsx, T, c.layer, out, base=base), kernel)
+    check_precision(c.run(F32), c.products()[0][0], K)
+
+
+@pytest.mark.parametrize("kernel,T,K,F,forms", [
+    ("fp8_stream_kernel<2, true, false>", 50, 2048, 5456, ("true", "false")),
+    ("fp8_stream_kernel<2, true, true>", 50, 2064, 5456, ("true", "false")),
+    ("fp8_stream_kernel<2, false, false>", 33, 512, 16384, ("true", "false")),
+    ("fp8_stream_kernel<2, false, true>", 33, 528, 16384, ("true", "false")),
+    ("fp8_pair_kernel<3>", 2600, 1040, 1040, ("false",)), ("fp8_pair_kernel<4>", 2600, 1040, 1040, ("true",))])
+def test_stream_and_pair_kernels_gated(kernel, T, K, F, forms):
+    check_gated(kernel, T, K, F, forms)
