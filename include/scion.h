@@ -398,7 +398,7 @@ size_t scion_fp8_device_bytes(const scion_fp8* layer);
  * [T][ceil(k/128)]), out device [T][n] of out_type (SCION_F32 or SCION_BF16), base device fp32
  * [T][n] or NULL; with out_type SCION_F32 it may be out itself.  Products and sums in fp32, one
  * rounding to out_type.  A row's result is bit-reproducible for the same T and does not depend on
- * the other rows.  0 <= T <= 2^21 (T = 0 is a no-op).  x_codes 16-byte aligned, out and base aligned to
+ * the other rows.  out overlaps no other argument except as said.  0 <= T <= 2^21 (T = 0 is a no-op).  x_codes 16-byte aligned, out and base aligned to
  * their elements.  The handle holds no workspace: calls on one handle may overlap.  EINVAL (also
  * for a gated layer), ECUDA. */
 int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* layer, const float* base,
@@ -406,8 +406,9 @@ int scion_fp8_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, co
 
 /* h_t = silu(W_gate x_t) * (W_up x_t) of a gated layer in one kernel: h_bf16 device bf16 [T][n] or
  * NULL; h_codes [T][n] and h_scales [T][ceil(n/128)], both or neither (quantized from the fp32 h,
- * ready as the x of the down projection); one of the two forms is given, not both.  h_bf16 and
- * h_codes 16-byte aligned.  Otherwise as scion_fp8_forward; EINVAL for a plain layer. */
+ * ready as the x of the down projection); one of the two forms is given, not both.  silu(g) of
+ * g < -87, at most 1.2e-36 in size, is taken as 0.  h_bf16 and h_codes 16-byte aligned, no output
+ * overlaps another argument.  Otherwise as scion_fp8_forward; EINVAL for a plain layer. */
 int scion_fp8_gated_forward(const uint8_t* x_codes, const uint8_t* x_scales, int T, const scion_fp8* layer,
                             void* h_bf16, uint8_t* h_codes, uint8_t* h_scales, void* stream);
 

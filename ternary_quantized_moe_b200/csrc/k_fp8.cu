@@ -43,7 +43,9 @@ typedef __nv_bfloat16 bf16;
 // reduction for a token's scale, 128 features in whole sectors.
 // Measured (replayed from a graph): 64 tokens, 16384 x 8192, 27.5 us (5.2 TB/s); 2048 x 4096 in clusters of
 // 4, 6.0 us, of which the K loop is two: start of the cluster, first copies, exchange and stores are the
-// rest.  A block of K of 128 takes 0.25 us (24 KB per SM: the rate of an SM's reads from L2).
+// rest.  A block of K of 128 takes 0.27 us with 64 tokens, bound by the MMA warp: 0.25 with the copies left
+// out of a copy of the kernel, 0.145 with the MMAs left out and 0.14 with neither (1000 tokens, 1112 rows, K
+// = 1024 and 2048; the four MMAs of a block are 0.1, waiting for stages and handing them over the rest).
 constexpr int kStreamThreads = 320;
 constexpr int kMaxStages = 8;
 // K blocks of 128 per stage: waiting for a stage takes as long as four narrow MMAs, so a stage holds
@@ -1013,10 +1015,14 @@ struct StreamPlan {
 // Tokens per tile: the accumulators (nw bn columns) and the scale words share 512 columns of tensor
 // memory, so 256 at most (208 for two matrices); narrower tiles give more CTAs, and tiles of up to
 // 128 / nw tokens can split K over a cluster.  The estimate is a fit to launches of 8 to 128 tiles of
-// 32 to 128 tokens, K = 2048 to 8192 (within 10%): a start that grows with the tile's tokens (they
-// pass the epilogue one warp each), with the cluster and with the share of the SMs in use, and a time
-// per block of K, which the issuing of its MMAs bounds up to 128 tokens.  Clusters that leave next to no SM
-// free start late: 1000 tokens, 1112 x 2048, take 8.6 us as 72 pairs of CTAs and 7.5 as 144 CTAs.
+// 32 to 128 tokens, K = 2048 to 8192: a start that grows with the tile's tokens (they pass the epilogue one
+// warp each), with the cluster and with the share of the SMs in use (a term without a cause found for it),
+// and a time per block of K, which the MMA warp bounds up to 128 tokens; weights that come from HBM are not
+// in it.  Clusters that leave next to no SM free start late: 1000 tokens, 1112 x 2048, take 8.6 us as 72
+// pairs of CTAs and 7.5 as 144 CTAs.  What it is good for is the choice: over 978 shapes (33 to 4096 tokens,
+// K = 256 to 8192, n = 512 to 16384, plain and gated, with and without a base) on both kernels, nine tenths
+// of the estimates are 0.71 to 1.17 of the time, and the kernel chosen is more than 5% behind the other in
+// 28, more than 10% in 12, 21% at most (gated, 128 tokens, 2 x 8192 x 512: 8.2 us, 6.8 streamed).
 StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
   StreamPlan best{};
   for (int most : {256, 128, 64}) {
@@ -1044,7 +1050,7 @@ StreamPlan plan_stream(const scion_fp8* L, int nw, int T, int N, int KB) {
   return best;
 }
 
-// The same for the pair kernel, fitted the same way.  A base costs a round of tiles about 4 us (it passes
+// The same for the pair kernel, fitted the same way (0.76 to 1.07 of the time).  A base costs a round of tiles about 4 us (it passes
 // through the shared memory that the next tile's MMAs read from), the streaming kernel less than one.
 double pair_us(const scion_fp8* L, int nw, int T, int N, int KB, bool base) {
   const int64_t tiles = int64_t((T + 255) / 256) * (nw == 1 ? (N + 255) / 256 : (N + 127) / 128);

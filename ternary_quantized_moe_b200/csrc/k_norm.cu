@@ -7,8 +7,8 @@
 // lanes; the loads of a warp cover whole 32-byte sectors.  Programmatic dependent launch lets a call's
 // blocks start as its predecessor's drain.  Replayed from a graph: the norm of 16384 x 4096 (bf16 + fp32
 // in, fp32 + 8 bits out, 738 MB) 106.7 us, 6.9 TB/s, and of one row of 2048 1.8 us; 8192 x 8192 fp32 in
-// 128 x 128 blocks 49.3 us, 6.8 TB/s; 16384 x 4096 bf16 by rows 37.3 us, 5.4 TB/s (issue slots 84% busy:
-// the conversions of two bytes of source to one).
+// 128 x 128 blocks 49.4 us, 6.8 TB/s, bf16 33.8 us, 6.0; 16384 x 4096 bf16 by rows 37.3 us, 5.4 TB/s (issue
+// slots 84% busy: the conversions of two bytes of source to one).
 #include <math.h>
 
 #include <algorithm>
@@ -170,8 +170,8 @@ cudaError_t launch_norm(const NormParams& p, int T, cudaStream_t s) {
   // 16384 rows of 128 fp32: 7 us with a warp per row, 17 with a CTA
   if (chunks <= 64) return launch_pdl(rmsnorm_warp_kernel<X, R, 2, kSmallEps>, dim3(unsigned((int64_t(T) + 7) / 8)), dim3(256), 0, s, p, T);
   // One chunk per thread is the quickest for few rows (1 x 4096 fp32: 2.2 us, 2.6 with two) and as good
-  // for many, except where a thread would read 16 bytes in all (16384 x 4096 bf16 without a residual: 66
-  // us, 54 with two) or the CTA have 1024 threads (8192 x 8192 bf16: 83 us, 80).
+  // for many, except where a thread would read 16 bytes in all (16384 x 4096 bf16 without a residual: 60
+  // us, 48 with two) or the CTA have 1024 threads (8192 x 8192 bf16 with a residual: 84 us, 83).
   const int cpt = chunks > 2048 ? 4 : chunks > 512 || (chunks > 256 && sizeof(X) == 2 && !p.resid) ? 2 : 1;
   const int nt = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
   if (cpt == 1) return launch_pdl(rmsnorm_kernel<X, R, 1, kSmallEps>, dim3(T), dim3(nt), 0, s, p);
